@@ -20,6 +20,9 @@
  * and the decode update on a 16-bit state with stochastic rounding: ssd_state_update_lp,
  * and the gated group RMSNorm of the mixer output: ssd_gated_rmsnorm,
  * and one decode step (conv update + state update) in one launch: ssd_decode_step
+ * and the per-channel form of the scan, with gradients, and the conv's gradient: ssd_selective_scan,
+ *   ssd_selective_scan_bwd, ssd_selective_state_update, ssd_conv1d_bwd
+ * and the slots of state pools: ssd_pool_copy, ssd_pool_clear, ssd_pool_compact
  *
  * Sources (web pages, cited by title and section):
  *  [P1] "Mamba 与 Nemotron 系列模型深度调研": "Mamba 架构 / 1. Selective SSM 的直觉"
@@ -554,6 +557,128 @@ ssd_status_t ssd_state_update_accept(const ssd_dims_t* d, float* state, const in
 ssd_status_t ssd_conv1d_update_accept(const ssd_dims_t* d, const void* xbc, int64_t xbc_row_stride, void* conv_state,
                                       const int32_t* slot_idx, int64_t nslots, const int32_t* accept_len,
                                       hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The per-channel selective scan ([P1] section 1, before heads share a decay): every channel has its
+ * own decay row and its own dt.  In ssd_dims_t the channels are the heads: nheads = D channels,
+ * head_dim = 1 (else SSD_ERR_SHAPE), D % ngroups == 0, d_state N 16, 32, 64 or 128 (else
+ * SSD_ERR_UNSUPPORTED); g(d) = d / (D/G).  Per batch entry and channel, in fp32 (b: batch entry):
+ *   S = exp(dt*A[d,:]) * S + dt*x * B[b,t,g(d),:]
+ *   y[b,t,d] = (<S, C[b,t,g(d),:]> + Dskip[d]*x) * (z ? silu(z[b,t,d]) : 1)
+ */
+
+/*
+ * Scan of a prefill.
+ *  x, z         [B, L, D] act dtype; token rows x_row_stride / z_row_stride elements apart (>= D),
+ *               batch rows L rows apart.  x may be the conv's output, z a view into in_proj's.  z may
+ *               be NULL (no gate; its stride is then not read).
+ *  dt           [B, L, D] contiguous act dtype.  dt_params as for ssd_chunk_scan, bias [D].
+ *  A            [D, N] fp32.  Dskip: [D] fp32 or NULL.
+ *  B, C         B[b,t,g,n] at B[(b*L + t)*bc_row_stride + g*N + n] (same for C); act dtype, 16-byte
+ *               aligned, bc_row_stride a multiple of 8 (bf16) or 4 (fp32).  May be views into a
+ *               projection's output.
+ *  init_state   [B, D, N] fp32, or NULL (zeros).  final_state [B, D, N] fp32, or NULL (not written);
+ *               may alias init_state.
+ *  y            [B, L, D] contiguous, y dtype.
+ *  workspace    as many bytes as ssd_selective_scan_workspace_size() returns, 16-byte aligned,
+ *               overwritten (may be NULL when that is 0; smaller: SSD_ERR_WORKSPACE).
+ */
+size_t ssd_selective_scan_workspace_size(const ssd_dims_t* d);
+ssd_status_t ssd_selective_scan(const ssd_dims_t* d, const void* x, int64_t x_row_stride, const void* dt,
+                                const float* A, const void* B, const void* C, int64_t bc_row_stride,
+                                const float* Dskip, const void* z, int64_t z_row_stride,
+                                const ssd_dt_params_t* dt_params, const float* init_state, float* final_state,
+                                void* y, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Its gradient, from the inputs alone (states are recomputed, nothing need be kept from the forward).
+ *  dy            [B, L, D] contiguous, y dtype: the gradient of y.
+ *  dfinal_state  [B, D, N] fp32: the gradient of final_state, or NULL (zeros).
+ *  dx, ddt, dz   [B, L, D] contiguous act dtype; ddt is the gradient of the stored dt, through the dt
+ *                prologue (a clamp passes it where lo <= value <= hi).  dz required with z, else unused.
+ *  dB, dC        [B, L, G, N] contiguous act dtype.
+ *  dA [D, N], dDskip [D], ddt_bias [D], dinit_state [B, D, N]: fp32; dDskip, ddt_bias and dinit_state
+ *                may be NULL (not written).
+ * Every gradient is overwritten, and is the same bit for bit on every call with the same inputs.
+ * Sums over tokens and channels are fp32.  A dB or dC term that is not finite spreads within its block
+ * of 16 (token, state) pairs.  The rest is as for ssd_selective_scan; a workspace of
+ * ssd_selective_scan_bwd_workspace_size() bytes is required.
+ */
+size_t ssd_selective_scan_bwd_workspace_size(const ssd_dims_t* d);
+ssd_status_t ssd_selective_scan_bwd(const ssd_dims_t* d, const void* dy, const void* x, int64_t x_row_stride,
+                                    const void* dt, const float* A, const void* B, const void* C,
+                                    int64_t bc_row_stride, const float* Dskip, const void* z, int64_t z_row_stride,
+                                    const ssd_dt_params_t* dt_params, const float* init_state,
+                                    const float* dfinal_state, void* dx, void* ddt, float* dA, void* dB, void* dC,
+                                    float* dDskip, void* dz, float* ddt_bias, float* dinit_state, void* workspace,
+                                    size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token per batch entry (d->seqlen is ignored).
+ *  state      [B or nslots, D, N] fp32, 16-byte aligned; state_out the same, and may be state (in
+ *             place) but not overlap it otherwise.  Only the entries or slots that the call names
+ *             are written.
+ *  slot_idx   [B] int32 device memory, or NULL (entry b), as ssd_state_update_lp: padding entries
+ *             start from zeros and store nothing, slots of one call are distinct.
+ *  x, z       rows of D channels x_row_stride / z_row_stride elements apart; dt [B, D] contiguous;
+ *             B, C rows bc_row_stride apart (no alignment needed); A 16-byte aligned.
+ *  y          [B, D] contiguous, y dtype.
+ */
+ssd_status_t ssd_selective_state_update(const ssd_dims_t* d, const float* state, float* state_out,
+                                        const int32_t* slot_idx, int64_t nslots, const void* x,
+                                        int64_t x_row_stride, const void* dt, const float* A, const void* B,
+                                        const void* C, int64_t bc_row_stride, const float* Dskip, const void* z,
+                                        int64_t z_row_stride, const ssd_dt_params_t* dt_params, void* y,
+                                        hipStream_t stream);
+
+/*
+ * Gradient of ssd_conv1d_fwd.
+ *  dout             [B, L, CD] contiguous act dtype: the gradient of out.
+ *  dconv_state_out  [B, CD, 4] act dtype: the gradient of conv_state_out, or NULL (zeros).
+ *  dxbc             [B, L, CD] contiguous act dtype.
+ *  dw [CD, 4], dbias [CD]: fp32, summed over batch and tokens in a fixed order; dbias may be NULL.
+ *  dconv_state_in   [B, CD, 4] act dtype, or NULL (not written).
+ *  workspace        ssd_conv1d_bwd_workspace_size() bytes, 16-byte aligned, overwritten.
+ * xbc, w, bias and conv_state_in as given to the forward; gradients must not overlap its buffers or
+ * one another.
+ */
+size_t ssd_conv1d_bwd_workspace_size(const ssd_dims_t* d);
+ssd_status_t ssd_conv1d_bwd(const ssd_dims_t* d, const void* xbc, int64_t xbc_row_stride, const void* w,
+                            const void* bias, const void* conv_state_in, const void* dout,
+                            const void* dconv_state_out, void* dxbc, float* dw, float* dbias, void* dconv_state_in,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Slots of state pools.  A pool here is `layers` arrays of slots, layer l at l * layer_stride bytes,
+ * slot s of a layer at s * slot_bytes: one call serves a pool of any type, and all layers of a model
+ * kept in one allocation.  Pools, slot_bytes and layer strides are multiples of 16 bytes
+ * (SSD_ERR_ALIGN); a layer stride holds at least its slots (SSD_ERR_SHAPE); layers <= 65535.
+ * Index tables are int32 device memory, read in stream order; entries that name no slot are skipped.
+ *
+ * ssd_pool_copy    for i = 0 .. n-1, in this order and in every layer: dst slot dst_idx[i] <- src slot
+ *                  src_idx[i].  The pools may be the same (forks, moves); otherwise they must not
+ *                  overlap, and then a snapshot pool is written or restored.  A source may occur any
+ *                  number of times.  Where a destination occurs twice or is another entry's source
+ *                  the copies run one after the other (same result as the order says, slower).
+ * ssd_pool_clear   zeroes the slots slot_idx[0 .. n-1] (freed ones, or before a decode-only start).
+ * ssd_pool_compact plans the moves that bring a pool's live slots to its front: slot_idx [n] names the
+ *                  live slots (repeats and padding allowed).  With `count` distinct live slots, those
+ *                  below count stay and the k-th live slot from count on moves to the k-th free slot
+ *                  below count.  Writes src_idx and dst_idx [n] (the moves in that order, then -1),
+ *                  new_slot_idx [n] (the table after the moves; padding unchanged) and count [1].
+ *                  ssd_pool_copy(pool, pool, src_idx, dst_idx) then makes the moves, in each pool
+ *                  that the table serves.  nslots <= 131072 (else SSD_ERR_UNSUPPORTED).  The four
+ *                  outputs must not overlap the input or one another.
+ */
+ssd_status_t ssd_pool_copy(void* dst_pool, int64_t dst_nslots, int64_t dst_layer_stride, const void* src_pool,
+                           int64_t src_nslots, int64_t src_layer_stride, int64_t slot_bytes, int64_t layers,
+                           const int32_t* dst_idx, const int32_t* src_idx, int64_t n, hipStream_t stream);
+ssd_status_t ssd_pool_clear(void* pool, int64_t nslots, int64_t layer_stride, int64_t slot_bytes, int64_t layers,
+                            const int32_t* slot_idx, int64_t n, hipStream_t stream);
+ssd_status_t ssd_pool_compact(const int32_t* slot_idx, int64_t n, int64_t nslots, int32_t* src_idx,
+                              int32_t* dst_idx, int32_t* new_slot_idx, int32_t* count, hipStream_t stream);
 
 /* Static, human-readable name of a status code. */
 const char* ssd_status_string(ssd_status_t s);

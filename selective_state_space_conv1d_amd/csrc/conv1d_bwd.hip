@@ -1,0 +1,176 @@
+// Gradient of the causal depthwise conv + SiLU (conv1d.hip).  With u~ the input preceded by the conv
+// state, p_t = bias + sum_k w[k] u~[t-3+k] and q_t = dout_t silu'(p_t):
+//   du~[t] = sum_k w[k] q[t+3-k]     dw[k] = sum_{b,t} q[t] u~[t-3+k]     dbias = sum_{b,t} q
+// The states' own gradients: conv_state_out[k] = u~[L-4+k] adds to du~, and conv_state_in's gradient is
+// du~ at the four positions before the first token (the oldest feeds no output).
+//
+// A thread owns one 16-byte vector of channels and walks a tile of tokens with the last three inputs
+// and q values in registers, so each input is read once (plus three rows on either side of a tile) and
+// each output written once: bound by HBM.  dw and dbias are summed in registers over the tile, over
+// the workgroup's tiles in LDS and over workgroups by a second launch, in a fixed order.
+#include "ssd_device.h"
+#include "ssd_kernels.h"
+
+namespace ssd {
+
+constexpr int kCbLanes = 64;     // channel vectors per workgroup
+constexpr int kCbSub = 4;        // token tiles per workgroup, one for each wave
+constexpr int kCbTokens = 64;    // tokens per tile
+
+template <typename T>
+__global__ __launch_bounds__(kCbLanes * kCbSub) void conv1d_bwd_kernel(ConvBwdArgs a, float* __restrict__ part,
+                                                                       int64_t tblocks, int64_t cblocks) {
+    constexpr int V = Vec16<T>::n;
+    __shared__ float red[kCbSub][5][V][kCbLanes];
+    const int lane = threadIdx.x % kCbLanes, sub = threadIdx.x / kCbLanes;
+    const int64_t cb = blockIdx.x % cblocks, tb = blockIdx.x / cblocks % tblocks, b = blockIdx.x / (cblocks * tblocks);
+    const int64_t CD = a.channels, L = a.seqlen;
+    const bool ok = (cb * kCbLanes + lane) * V < CD;
+    const int64_t c0 = ok ? (cb * kCbLanes + lane) * V : 0;
+    const int64_t t0 = (tb * kCbSub + sub) * kCbTokens;
+    const int64_t t1 = t0 + kCbTokens < L ? t0 + kCbTokens : L;
+    const T* xp = static_cast<const T*>(a.xbc) + b * L * a.xbc_row_stride + c0;
+    const T* gp = static_cast<const T*>(a.dout) + b * L * CD + c0;
+    T* dp = static_cast<T*>(a.dxbc) + b * L * CD + c0;
+    const T* sin = a.state_in ? static_cast<const T*>(a.state_in) + (b * CD + c0) * 4 : nullptr;
+    const T* dso = a.dstate_out ? static_cast<const T*>(a.dstate_out) + (b * CD + c0) * 4 : nullptr;
+    T* dsi = a.dstate_in ? static_cast<T*>(a.dstate_in) + (b * CD + c0) * 4 : nullptr;
+    float wt[4][V], bs[V], dw[4][V], db[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        bs[v] = a.bias ? static_cast<float>(static_cast<const T*>(a.bias)[c0 + v]) : 0.f;
+        db[v] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            wt[k][v] = static_cast<float>(static_cast<const T*>(a.w)[(c0 + v) * 4 + k]);
+            dw[k][v] = 0.f;
+        }
+    }
+    // du~[t] from outside the outputs: the stored windows
+    auto stored = [&](int64_t t, int v) { return dso && t >= L - 4 ? static_cast<float>(dso[v * 4 + (t - L + 4)]) : 0.f; };
+    if (ok && t0 < t1) {
+        float u0[V], u1[V], u2[V], q1[V], q2[V], q3[V];   // u~[t-3..t-1]; q[t-1], q[t-2], q[t-3]
+        auto input = [&](int64_t t, float (&o)[V]) {
+            if (t >= 0) load16_f32(xp + t * a.xbc_row_stride, o);
+            else
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] = sin ? static_cast<float>(sin[v * 4 + 4 + t]) : 0.f;
+        };
+        input(t0 - 3, u0);
+        input(t0 - 2, u1);
+        input(t0 - 1, u2);
+#pragma unroll
+        for (int v = 0; v < V; ++v) q1[v] = q2[v] = q3[v] = 0.f;
+        // q of three tokens past the tile are needed for its last inputs; past L they are 0
+        for (int64_t t = t0; t < t1 + 3; ++t) {
+            float u3[V], go[V], q[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) u3[v] = go[v] = 0.f;
+            if (t < L) {
+                load16_f32(xp + t * a.xbc_row_stride, u3);
+                load16_f32(gp + t * CD, go);
+            }
+            float du[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float p = fmaf(wt[3][v], u3[v], fmaf(wt[2][v], u2[v], fmaf(wt[1][v], u1[v], fmaf(wt[0][v], u0[v], bs[v]))));
+                const float sg = __builtin_amdgcn_rcpf(1.f + __expf(-p));
+                q[v] = t < L ? go[v] * sg * fmaf(p, 1.f - sg, 1.f) : 0.f;
+                if (t < t1) {
+                    dw[0][v] = fmaf(q[v], u0[v], dw[0][v]);
+                    dw[1][v] = fmaf(q[v], u1[v], dw[1][v]);
+                    dw[2][v] = fmaf(q[v], u2[v], dw[2][v]);
+                    dw[3][v] = fmaf(q[v], u3[v], dw[3][v]);
+                    db[v] += q[v];
+                }
+                du[v] = fmaf(wt[3][v], q3[v], fmaf(wt[2][v], q2[v], fmaf(wt[1][v], q1[v], wt[0][v] * q[v])));
+                u0[v] = u1[v];
+                u1[v] = u2[v];
+                u2[v] = u3[v];
+                q3[v] = q2[v];
+                q2[v] = q1[v];
+                q1[v] = q[v];
+            }
+            // du belongs to token t - 3; before the tile's first token the earlier tile owns it, and
+            // before the sequence's first it is the conv state's
+            const int64_t r = t - 3;
+            if (dso && r >= L - 4)
+#pragma unroll
+                for (int v = 0; v < V; ++v) du[v] += stored(r, v);
+            if (r >= t0) store16_f32(dp + r * CD, du);
+            else if (t0 == 0 && dsi)
+#pragma unroll
+                for (int v = 0; v < V; ++v) dsi[v * 4 + 4 + r] = static_cast<T>(du[v]);
+        }
+        if (t0 == 0 && dsi)
+#pragma unroll
+            for (int v = 0; v < V; ++v) dsi[v * 4] = static_cast<T>(stored(-4, v));
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) red[sub][k][v][lane] = dw[k][v];
+        red[sub][4][v][lane] = db[v];
+    }
+    __syncthreads();
+    // part[(b, tb)][5][CD]
+    float* pp = part + (b * tblocks + tb) * 5 * CD;
+    for (int i = threadIdx.x; i < 5 * V * kCbLanes; i += kCbLanes * kCbSub) {
+        const int k = i / (V * kCbLanes), cc = i % (V * kCbLanes);
+        const int64_t c = cb * kCbLanes * V + cc;
+        if (c >= CD) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int j = 0; j < kCbSub; ++j) v += red[j][k][cc % V][cc / V];
+        pp[k * CD + c] = v;
+    }
+}
+
+// Sums of part over its n rows: dw[c][k] and dbias[c].
+__global__ __launch_bounds__(256) void conv1d_bwd_sums_kernel(const float* __restrict__ part, int64_t n, int64_t CD,
+                                                              float* __restrict__ dw, float* __restrict__ dbias) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= 5 * CD) return;
+    float v = 0.f;
+    for (int64_t r = 0; r < n; ++r) v += part[r * 5 * CD + i];
+    const int64_t k = i / CD, c = i % CD;
+    if (k < 4) dw[c * 4 + k] = v;
+    else if (dbias) dbias[c] = v;
+}
+
+// L = 0: the conv state's gradient is the stored one's.
+template <typename T>
+__global__ __launch_bounds__(256) void conv1d_bwd_state_kernel(const T* __restrict__ dso, T* __restrict__ dsi, int64_t n) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i < n) dsi[i] = dso ? dso[i] : static_cast<T>(0.f);
+}
+
+static int64_t token_blocks(int64_t L) { return (L + kCbTokens * kCbSub - 1) / (kCbTokens * kCbSub); }
+
+size_t conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t channels, Dt act) {
+    return static_cast<size_t>(batch * token_blocks(seqlen) * 5 * channels) * sizeof(float);
+}
+
+template <typename T>
+static hipError_t conv_bwd_t(const ConvBwdArgs& a, float* part, hipStream_t s) {
+    constexpr int V = Vec16<T>::n;
+    const int64_t tb = token_blocks(a.seqlen), cb = (a.channels + kCbLanes * V - 1) / (kCbLanes * V);
+    const int64_t blocks = a.batch * tb * cb;
+    if (blocks > 0)
+        hipLaunchKernelGGL((conv1d_bwd_kernel<T>), dim3(static_cast<uint32_t>(blocks)), dim3(kCbLanes * kCbSub), 0, s, a, part, tb, cb);
+    else if (a.batch > 0 && a.dstate_in) {
+        const int64_t n = a.batch * a.channels * 4;
+        hipLaunchKernelGGL((conv1d_bwd_state_kernel<T>), dim3(static_cast<uint32_t>((n + 255) / 256)), dim3(256), 0, s,
+                           static_cast<const T*>(a.dstate_out), static_cast<T*>(a.dstate_in), n);
+    }
+    hipLaunchKernelGGL(conv1d_bwd_sums_kernel, dim3(static_cast<uint32_t>((5 * a.channels + 255) / 256)), dim3(256), 0, s,
+                       part, a.batch * tb, a.channels, a.dw, a.dbias);
+    return hipGetLastError();
+}
+
+hipError_t launch_conv1d_bwd(const ConvBwdArgs& a, Dt act, void* workspace, hipStream_t s) {
+    float* part = static_cast<float*>(workspace);
+    return act == Dt::BF16 ? conv_bwd_t<bf16>(a, part, s) : conv_bwd_t<float>(a, part, s);
+}
+
+}  // namespace ssd

@@ -45,6 +45,46 @@ ssd_status_t check_seq_tables(const ssd_dims_t* d, const int32_t* cu_seqlens, co
     return SSD_OK;
 }
 
+// The per-channel selective scan: the channels are the heads.
+ssd_status_t check_selective(const ssd_dims_t* d, bool need_seqlen) {
+    ssd_status_t st = check_dims(d, need_seqlen);
+    if (st != SSD_OK) return st;
+    if (d->head_dim != 1) return SSD_ERR_SHAPE;
+    if (!pow2_16_128(d->d_state)) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+// Sizes whose workgroup counts and element counts fit the launches: rows x channel blocks and the
+// gradient's sums below 2^31 workgroups, batch and rows below 2^31.
+bool selective_sizes_ok(const ssd_dims_t* d, int64_t seqlen) {
+    constexpr int64_t kMax = INT32_MAX;
+    if (d->batch > kMax || seqlen > kMax || (seqlen > 0 && d->batch > (INT64_C(1) << 40) / seqlen)) return false;
+    const int64_t blocks = static_cast<int64_t>(d->ngroups) * ((d->nheads / d->ngroups + 63) / 64);
+    if (d->batch > 0 && blocks > kMax / d->batch) return false;
+    const int64_t per_row = 2LL * d->ngroups * d->d_state, params = (d->d_state + 2LL) * d->nheads;
+    const int64_t rows = d->batch * seqlen;
+    return rows == 0 || (kMax * 256LL - params) / per_row >= rows;
+}
+ssd_status_t check_workspace(const void* p, size_t have, size_t need) {
+    if (need == 0) return SSD_OK;
+    if (!p || have < need) return SSD_ERR_WORKSPACE;
+    return aligned16(p) ? SSD_OK : SSD_ERR_ALIGN;
+}
+// elements aligned to their own size
+bool aligned_to(const void* p, int32_t dt) { return reinterpret_cast<uintptr_t>(p) % elem_size(dt) == 0; }
+
+// A pool's geometry and an index table.
+ssd_status_t check_pool(const void* pool, int64_t nslots, int64_t layer_stride, int64_t slot_bytes, int64_t layers) {
+    if (nslots < 0 || layers < 0 || slot_bytes < 0 || layer_stride < 0) return SSD_ERR_SHAPE;
+    if (nslots > INT32_MAX || layers > 65535) return SSD_ERR_UNSUPPORTED;
+    if (nslots > 0 && slot_bytes > INT64_MAX / nslots) return SSD_ERR_SHAPE;
+    if (layers > 1 && layer_stride < nslots * slot_bytes) return SSD_ERR_SHAPE;
+    if (nslots > 0 && layers > 0 && slot_bytes > 0 && !pool) return SSD_ERR_NULL;
+    if (slot_bytes % 16 != 0 || (layers > 1 && layer_stride % 16 != 0) || (pool && !aligned16(pool))) return SSD_ERR_ALIGN;
+    return SSD_OK;
+}
+// workgroups of a copy: one for every 32 KiB of every entry
+bool pool_grid_ok(int64_t n, int64_t slot_bytes) { return n <= INT32_MAX && (n == 0 || slot_bytes / 32768 + 1 <= INT32_MAX / n); }
+
 }  // namespace
 
 extern "C" {
@@ -641,6 +681,179 @@ ssd_status_t ssd_decode_step(const ssd_dims_t* d, const void* xbc, int64_t xbc_r
                            d->ngroups, d->d_state, nullptr, 0, dt_params_of(dt_params)},
                           xbc, xbc_row_stride, w, bias, conv_state_in, conv_state_out};
     return hip_status(ssd::launch_decode_step(a, static_cast<Dt>(d->act_dtype), static_cast<Dt>(d->y_dtype), stream));
+}
+
+size_t ssd_selective_scan_workspace_size(const ssd_dims_t* d) {
+    if (check_selective(d, true) != SSD_OK || !selective_sizes_ok(d, d->seqlen)) return 0;
+    return ssd::selective_scan_workspace_bytes(d->batch, d->seqlen, d->nheads, d->ngroups, d->d_state);
+}
+
+ssd_status_t ssd_selective_scan(const ssd_dims_t* d, const void* x, int64_t x_row_stride, const void* dt,
+                                const float* A, const void* B, const void* C, int64_t bc_row_stride,
+                                const float* Dskip, const void* z, int64_t z_row_stride,
+                                const ssd_dt_params_t* dt_params, const float* init_state, float* final_state,
+                                void* y, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    ssd_status_t st = check_selective(d, true);
+    if (st != SSD_OK) return st;
+    const bool tokens = d->batch > 0 && d->seqlen > 0;
+    if (d->batch > 0 && !A) return SSD_ERR_NULL;
+    if (tokens && (!x || !dt || !B || !C || !y)) return SSD_ERR_NULL;
+    if (!selective_sizes_ok(d, d->seqlen)) return SSD_ERR_UNSUPPORTED;
+    const int64_t GN = static_cast<int64_t>(d->ngroups) * d->d_state;
+    if (tokens && (x_row_stride < d->nheads || bc_row_stride < GN || (z && z_row_stride < d->nheads))) return SSD_ERR_SHAPE;
+    if (tokens && !stride_ok(bc_row_stride, d->act_dtype)) return SSD_ERR_ALIGN;
+    for (const void* p : {B, C})
+        if (p && !aligned16(p)) return SSD_ERR_ALIGN;
+    for (const void* p : {x, dt, z})
+        if (p && !aligned_to(p, d->act_dtype)) return SSD_ERR_ALIGN;
+    if (y && !aligned_to(y, d->y_dtype)) return SSD_ERR_ALIGN;
+    for (const void* p : {static_cast<const void*>(A), static_cast<const void*>(Dskip), static_cast<const void*>(init_state),
+                          static_cast<const void*>(final_state)})
+        if (p && !aligned_to(p, SSD_F32)) return SSD_ERR_ALIGN;
+    if (!dt_params_ok(dt_params)) return SSD_ERR_ALIGN;
+    st = check_workspace(workspace, workspace_bytes, ssd_selective_scan_workspace_size(d));
+    if (st != SSD_OK) return st;
+    ssd::SelScanArgs a{x, x_row_stride, dt, A, B, C, bc_row_stride, Dskip, z, z_row_stride, init_state, final_state, y,
+                       d->batch, d->seqlen, d->nheads, d->ngroups, d->d_state, dt_params_of(dt_params)};
+    return hip_status(ssd::launch_selective_scan(a, static_cast<Dt>(d->act_dtype), static_cast<Dt>(d->y_dtype), workspace,
+                                                 stream));
+}
+
+size_t ssd_selective_scan_bwd_workspace_size(const ssd_dims_t* d) {
+    if (check_selective(d, true) != SSD_OK || !selective_sizes_ok(d, d->seqlen)) return 0;
+    return ssd::selective_bwd_workspace_bytes(d->batch, d->seqlen, d->nheads, d->ngroups, d->d_state);
+}
+
+ssd_status_t ssd_selective_scan_bwd(const ssd_dims_t* d, const void* dy, const void* x, int64_t x_row_stride,
+                                    const void* dt, const float* A, const void* B, const void* C,
+                                    int64_t bc_row_stride, const float* Dskip, const void* z, int64_t z_row_stride,
+                                    const ssd_dt_params_t* dt_params, const float* init_state,
+                                    const float* dfinal_state, void* dx, void* ddt, float* dA, void* dB, void* dC,
+                                    float* dDskip, void* dz, float* ddt_bias, float* dinit_state, void* workspace,
+                                    size_t workspace_bytes, hipStream_t stream) {
+    ssd_status_t st = check_selective(d, true);
+    if (st != SSD_OK) return st;
+    const bool tokens = d->batch > 0 && d->seqlen > 0;
+    if (!A || !dA) return SSD_ERR_NULL;
+    if (tokens && (!dy || !x || !dt || !B || !C || !dx || !ddt || !dB || !dC || (z && !dz))) return SSD_ERR_NULL;
+    if (!selective_sizes_ok(d, d->seqlen)) return SSD_ERR_UNSUPPORTED;
+    const int64_t GN = static_cast<int64_t>(d->ngroups) * d->d_state;
+    if (tokens && (x_row_stride < d->nheads || bc_row_stride < GN || (z && z_row_stride < d->nheads))) return SSD_ERR_SHAPE;
+    if (tokens && !stride_ok(bc_row_stride, d->act_dtype)) return SSD_ERR_ALIGN;
+    for (const void* p : {B, C})
+        if (p && !aligned16(p)) return SSD_ERR_ALIGN;
+    for (const void* p : {x, dt, z, static_cast<const void*>(dx), static_cast<const void*>(ddt), static_cast<const void*>(dB),
+                          static_cast<const void*>(dC), static_cast<const void*>(dz)})
+        if (p && !aligned_to(p, d->act_dtype)) return SSD_ERR_ALIGN;
+    if (dy && !aligned_to(dy, d->y_dtype)) return SSD_ERR_ALIGN;
+    for (const float* p : {A, Dskip, init_state, dfinal_state, static_cast<const float*>(dA), static_cast<const float*>(dDskip),
+                           static_cast<const float*>(ddt_bias), static_cast<const float*>(dinit_state)})
+        if (p && !aligned_to(p, SSD_F32)) return SSD_ERR_ALIGN;
+    if (!dt_params_ok(dt_params)) return SSD_ERR_ALIGN;
+    st = check_workspace(workspace, workspace_bytes, ssd_selective_scan_bwd_workspace_size(d));
+    if (st != SSD_OK) return st;
+    ssd::SelBwdArgs a{dy, x, x_row_stride, dt, A, B, C, bc_row_stride, Dskip, z, z_row_stride, init_state, dfinal_state,
+                      dx, ddt, dA, dB, dC, dDskip, dz, ddt_bias, dinit_state, d->batch, d->seqlen, d->nheads, d->ngroups,
+                      d->d_state, dt_params_of(dt_params)};
+    return hip_status(ssd::launch_selective_scan_bwd(a, static_cast<Dt>(d->act_dtype), static_cast<Dt>(d->y_dtype),
+                                                     workspace, stream));
+}
+
+ssd_status_t ssd_selective_state_update(const ssd_dims_t* d, const float* state, float* state_out,
+                                        const int32_t* slot_idx, int64_t nslots, const void* x,
+                                        int64_t x_row_stride, const void* dt, const float* A, const void* B,
+                                        const void* C, int64_t bc_row_stride, const float* Dskip, const void* z,
+                                        int64_t z_row_stride, const ssd_dt_params_t* dt_params, void* y,
+                                        hipStream_t stream) {
+    ssd_status_t st = check_selective(d, false);
+    if (st != SSD_OK) return st;
+    if (nslots < 0) return SSD_ERR_SHAPE;
+    if (d->batch > 0 && (!x || !dt || !A || !B || !C || !y)) return SSD_ERR_NULL;
+    if (d->batch > 0 && (!state || !state_out) && (!slot_idx || nslots > 0)) return SSD_ERR_NULL;
+    if (!selective_sizes_ok(d, 1)) return SSD_ERR_UNSUPPORTED;
+    const int64_t GN = static_cast<int64_t>(d->ngroups) * d->d_state;
+    if (d->batch > 0 && (x_row_stride < d->nheads || bc_row_stride < GN || (z && z_row_stride < d->nheads))) return SSD_ERR_SHAPE;
+    for (const void* p : {static_cast<const void*>(state), static_cast<const void*>(state_out), static_cast<const void*>(A)})
+        if (p && !aligned16(p)) return SSD_ERR_ALIGN;
+    for (const void* p : {x, dt, B, C, z})
+        if (p && !aligned_to(p, d->act_dtype)) return SSD_ERR_ALIGN;
+    if ((y && !aligned_to(y, d->y_dtype)) || (Dskip && !aligned_to(Dskip, SSD_F32)) || !dt_params_ok(dt_params)) return SSD_ERR_ALIGN;
+    ssd::SelUpdateArgs a{state, state_out, slot_idx, slot_idx ? nslots : d->batch, x, x_row_stride, dt, A, B, C,
+                         bc_row_stride, Dskip, z, z_row_stride, y, d->batch, d->nheads, d->ngroups, d->d_state,
+                         dt_params_of(dt_params), 0};
+    return hip_status(ssd::launch_selective_update(a, static_cast<Dt>(d->act_dtype), static_cast<Dt>(d->y_dtype), stream));
+}
+
+size_t ssd_conv1d_bwd_workspace_size(const ssd_dims_t* d) {
+    if (check_dims(d, true) != SSD_OK || d->batch > INT32_MAX || d->seqlen > INT32_MAX) return 0;
+    return ssd::conv1d_bwd_workspace_bytes(d->batch, d->seqlen, ssd_conv_dim(d), static_cast<Dt>(d->act_dtype));
+}
+
+ssd_status_t ssd_conv1d_bwd(const ssd_dims_t* d, const void* xbc, int64_t xbc_row_stride, const void* w,
+                            const void* bias, const void* conv_state_in, const void* dout,
+                            const void* dconv_state_out, void* dxbc, float* dw, float* dbias, void* dconv_state_in,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    ssd_status_t st = check_dims(d, true);
+    if (st != SSD_OK) return st;
+    const int64_t CD = ssd_conv_dim(d);
+    const bool tokens = d->batch > 0 && d->seqlen > 0;
+    if (!dw || (tokens && (!xbc || !w || !dout || !dxbc))) return SSD_ERR_NULL;
+    if (CD % 8 != 0) return SSD_ERR_UNSUPPORTED;
+    // workgroups (512 channels or fewer x 256 tokens) below 2^31
+    if (d->batch > INT32_MAX || d->seqlen > INT32_MAX ||
+        (d->batch > 0 && (d->seqlen / 256 + 1) * (CD / 256 + 1) > INT32_MAX / d->batch)) return SSD_ERR_UNSUPPORTED;
+    if (tokens && xbc_row_stride < CD) return SSD_ERR_SHAPE;
+    if (tokens && !stride_ok(xbc_row_stride, d->act_dtype)) return SSD_ERR_ALIGN;
+    for (const void* p : {xbc, w, bias, conv_state_in, dout, dconv_state_out, static_cast<const void*>(dxbc),
+                          static_cast<const void*>(dw), static_cast<const void*>(dbias),
+                          static_cast<const void*>(dconv_state_in)})
+        if (p && !aligned16(p)) return SSD_ERR_ALIGN;
+    st = check_workspace(workspace, workspace_bytes, ssd_conv1d_bwd_workspace_size(d));
+    if (st != SSD_OK) return st;
+    ssd::ConvBwdArgs a{xbc, xbc_row_stride, w, bias, conv_state_in, dout, dconv_state_out, dxbc, dw, dbias,
+                       dconv_state_in, d->batch, d->seqlen, CD};
+    return hip_status(ssd::launch_conv1d_bwd(a, static_cast<Dt>(d->act_dtype), workspace, stream));
+}
+
+ssd_status_t ssd_pool_copy(void* dst_pool, int64_t dst_nslots, int64_t dst_layer_stride, const void* src_pool,
+                           int64_t src_nslots, int64_t src_layer_stride, int64_t slot_bytes, int64_t layers,
+                           const int32_t* dst_idx, const int32_t* src_idx, int64_t n, hipStream_t stream) {
+    if (n < 0) return SSD_ERR_SHAPE;
+    ssd_status_t st = check_pool(dst_pool, dst_nslots, dst_layer_stride, slot_bytes, layers);
+    if (st == SSD_OK) st = check_pool(src_pool, src_nslots, src_layer_stride, slot_bytes, layers);
+    if (st != SSD_OK) return st;
+    if (n > 0 && (!dst_idx || !src_idx)) return SSD_ERR_NULL;
+    if (!pool_grid_ok(n, slot_bytes)) return SSD_ERR_UNSUPPORTED;
+    if (dst_nslots == 0 || src_nslots == 0) return SSD_OK;   // every entry is padding
+    // one pool, or two that do not overlap
+    const bool same = dst_pool == src_pool && (layers <= 1 || dst_layer_stride == src_layer_stride);
+    const uintptr_t d0 = reinterpret_cast<uintptr_t>(dst_pool), s0 = reinterpret_cast<uintptr_t>(src_pool);
+    const uintptr_t d1 = d0 + (layers > 0 ? layers - 1 : 0) * dst_layer_stride + dst_nslots * slot_bytes;
+    const uintptr_t s1 = s0 + (layers > 0 ? layers - 1 : 0) * src_layer_stride + src_nslots * slot_bytes;
+    if (!same && d0 < s1 && s0 < d1) return SSD_ERR_SHAPE;
+    ssd::PoolCopyArgs a{dst_pool, dst_nslots, layers > 1 ? dst_layer_stride : 0, src_pool, src_nslots,
+                        layers > 1 ? src_layer_stride : 0, slot_bytes, layers, n, dst_idx, src_idx};
+    return hip_status(ssd::launch_pool_copy(a, stream));
+}
+
+ssd_status_t ssd_pool_clear(void* pool, int64_t nslots, int64_t layer_stride, int64_t slot_bytes, int64_t layers,
+                            const int32_t* slot_idx, int64_t n, hipStream_t stream) {
+    if (n < 0) return SSD_ERR_SHAPE;
+    ssd_status_t st = check_pool(pool, nslots, layer_stride, slot_bytes, layers);
+    if (st != SSD_OK) return st;
+    if (n > 0 && !slot_idx) return SSD_ERR_NULL;
+    if (!pool_grid_ok(n, slot_bytes)) return SSD_ERR_UNSUPPORTED;
+    if (nslots == 0) return SSD_OK;
+    ssd::PoolCopyArgs a{pool, nslots, layers > 1 ? layer_stride : 0, nullptr, 0, 0, slot_bytes, layers, n, slot_idx, nullptr};
+    return hip_status(ssd::launch_pool_copy(a, stream));
+}
+
+ssd_status_t ssd_pool_compact(const int32_t* slot_idx, int64_t n, int64_t nslots, int32_t* src_idx,
+                              int32_t* dst_idx, int32_t* new_slot_idx, int32_t* count, hipStream_t stream) {
+    if (n < 0 || nslots < 0) return SSD_ERR_SHAPE;
+    if (!count || (n > 0 && (!slot_idx || !src_idx || !dst_idx || !new_slot_idx))) return SSD_ERR_NULL;
+    if (nslots > ssd::kPoolMaxSlots || n > INT32_MAX) return SSD_ERR_UNSUPPORTED;
+    return hip_status(ssd::launch_pool_compact(slot_idx, n, nslots, src_idx, dst_idx, new_slot_idx, count, stream));
 }
 
 }  // extern "C"

@@ -135,7 +135,80 @@ struct AcceptArgs {
     void* conv_state; const void* inter_conv; int64_t conv_bytes;
 };
 
+// Gradient of the prefill conv.  dbias, dw: fp32; NULL state pointers skip what they stand for.
+struct ConvBwdArgs {
+    const void* xbc; int64_t xbc_row_stride;
+    const void* w; const void* bias;
+    const void* state_in; const void* dout; const void* dstate_out;
+    void* dxbc; float* dw; float* dbias; void* dstate_in;
+    int64_t batch, seqlen, channels;
+};
+
+// The per-channel selective scan (selective_scan.hip): channels D in ngroups groups of B and C.
+struct SelScanArgs {
+    const void* x; int64_t x_row_stride;
+    const void* dt; const float* A;
+    const void* B; const void* C; int64_t bc_row_stride;
+    const float* D;
+    const void* z; int64_t z_row_stride;   // gate, or NULL
+    const float* init_state; float* final_state;
+    void* y;
+    int64_t batch, seqlen;
+    int channels, ngroups, d_state;
+    DtParams dtp;
+};
+
+// Its gradient: dy has the y dtype, dx, ddt, dz, dB and dC the activation dtype.
+struct SelBwdArgs {
+    const void* dy;
+    const void* x; int64_t x_row_stride;
+    const void* dt; const float* A;
+    const void* B; const void* C; int64_t bc_row_stride;
+    const float* D;
+    const void* z; int64_t z_row_stride;
+    const float* init_state; const float* dfinal_state;
+    void* dx; void* ddt; float* dA; void* dB; void* dC; float* dD; void* dz; float* ddt_bias; float* dinit_state;
+    int64_t batch, seqlen;
+    int channels, ngroups, d_state;
+    DtParams dtp;
+};
+
+// One token per batch entry; state_out may be state.
+struct SelUpdateArgs {
+    const float* state; float* state_out;
+    const int32_t* slot_idx; int64_t nslots;   // as UpdateArgs
+    const void* x; int64_t x_row_stride;
+    const void* dt; const float* A;
+    const void* B; const void* C; int64_t bc_row_stride;
+    const float* D;
+    const void* z; int64_t z_row_stride;
+    void* y;
+    int64_t batch;
+    int channels, ngroups, d_state;
+    DtParams dtp;
+    int64_t per_block;   // set by the launcher: batch entries per workgroup
+};
+
+// Slots of a pool copied into slots of a pool, in every layer; src NULL clears them.
+struct PoolCopyArgs {
+    void* dst; int64_t dst_slots, dst_layer_bytes;
+    const void* src; int64_t src_slots, src_layer_bytes;
+    int64_t slot_bytes, layers, n;
+    const int32_t* dst_idx; const int32_t* src_idx;
+};
+
 hipError_t launch_conv1d_fwd(const ConvFwdArgs& a, Dt act, hipStream_t s);
+size_t conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t channels, Dt act);
+hipError_t launch_conv1d_bwd(const ConvBwdArgs& a, Dt act, void* workspace, hipStream_t s);
+size_t selective_scan_workspace_bytes(int64_t batch, int64_t seqlen, int channels, int ngroups, int d_state);
+hipError_t launch_selective_scan(const SelScanArgs& a, Dt act, Dt ydt, void* workspace, hipStream_t s);
+size_t selective_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int channels, int ngroups, int d_state);
+hipError_t launch_selective_scan_bwd(const SelBwdArgs& a, Dt act, Dt ydt, void* workspace, hipStream_t s);
+hipError_t launch_selective_update(const SelUpdateArgs& a, Dt act, Dt ydt, hipStream_t s);
+hipError_t launch_pool_copy(const PoolCopyArgs& a, hipStream_t s);
+constexpr int64_t kPoolMaxSlots = 131072;   // the compaction's slot bitmap and its prefix counts fit in LDS
+hipError_t launch_pool_compact(const int32_t* slot_idx, int64_t n, int64_t nslots, int32_t* src_idx,
+                               int32_t* dst_idx, int32_t* new_idx, int32_t* count, hipStream_t s);
 // varlen prefill conv: the per-token pass, then the conv-state pass
 hipError_t launch_conv1d_fwd_varlen(const ConvFwdArgs& a, Dt act, hipStream_t s);
 hipError_t launch_conv1d_update(const ConvUpdateArgs& a, Dt act, hipStream_t s);

@@ -26,7 +26,9 @@ EXPORTS = ["ssd_conv_dim", "ssd_conv1d_fwd", "ssd_conv1d_update", "ssd_chunk_sca
            "ssd_chunk_scan_snapshots", "ssd_gated_rmsnorm", "ssd_decode_step", "ssd_state_update_accept",
            "ssd_conv1d_update_accept", "ssd_chunk_scan_varlen_snapshots", "ssd_chunk_scan_noalloc",
            "ssd_conv_chunk_scan", "ssd_chunk_scan_lp", "ssd_chunk_scan_varlen_lp",
-           "ssd_chunk_scan_varlen_workspace_size"]
+           "ssd_chunk_scan_varlen_workspace_size", "ssd_selective_scan_workspace_size", "ssd_selective_scan",
+           "ssd_selective_scan_bwd_workspace_size", "ssd_selective_scan_bwd", "ssd_selective_state_update",
+           "ssd_conv1d_bwd_workspace_size", "ssd_conv1d_bwd", "ssd_pool_copy", "ssd_pool_clear", "ssd_pool_compact"]
 
 
 class SsdDims(ctypes.Structure):
@@ -109,6 +111,25 @@ def _lib():
                                           _I32, _PSR, _VP, _VP, ctypes.c_size_t, _VP]
         lib.ssd_chunk_scan_varlen_lp.argtypes = [_PD, _I32, _VP, _I64, _VP, _VP, _I64, _VP, _VP, _VP, _PDT, _VP,
                                                  _VP, _VP, _VP, _I32, _I64, _PSR, _VP, _VP, ctypes.c_size_t, _VP]
+        for f in ("ssd_selective_scan_workspace_size", "ssd_selective_scan_bwd_workspace_size",
+                  "ssd_conv1d_bwd_workspace_size"):
+            getattr(lib, f).argtypes = [_PD]
+            getattr(lib, f).restype = ctypes.c_size_t
+        lib.ssd_selective_scan.argtypes = [_PD, _VP, _I64, _VP, _VP, _VP, _VP, _I64, _VP, _VP, _I64, _PDT, _VP, _VP,
+                                           _VP, _VP, ctypes.c_size_t, _VP]
+        lib.ssd_selective_scan_bwd.argtypes = [_PD, _VP, _VP, _I64, _VP, _VP, _VP, _VP, _I64, _VP, _VP, _I64, _PDT,
+                                               _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                                               ctypes.c_size_t, _VP]
+        lib.ssd_selective_state_update.argtypes = [_PD, _VP, _VP, _VP, _I64, _VP, _I64, _VP, _VP, _VP, _VP, _I64, _VP,
+                                                   _VP, _I64, _PDT, _VP, _VP]
+        lib.ssd_conv1d_bwd.argtypes = [_PD, _VP, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                                       ctypes.c_size_t, _VP]
+        lib.ssd_pool_copy.argtypes = [_VP, _I64, _I64, _VP, _I64, _I64, _I64, _I64, _VP, _VP, _I64, _VP]
+        lib.ssd_pool_clear.argtypes = [_VP, _I64, _I64, _I64, _I64, _VP, _I64, _VP]
+        lib.ssd_pool_compact.argtypes = [_VP, _I64, _I64, _VP, _VP, _VP, _VP, _VP]
+        for f in ("ssd_selective_scan", "ssd_selective_scan_bwd", "ssd_selective_state_update", "ssd_conv1d_bwd",
+                  "ssd_pool_copy", "ssd_pool_clear", "ssd_pool_compact"):
+            getattr(lib, f).restype = ctypes.c_int
         for f in ("ssd_conv1d_fwd", "ssd_conv1d_update", "ssd_chunk_scan", "ssd_state_update",
                   "ssd_conv1d_fwd_varlen", "ssd_conv1d_update_slots", "ssd_chunk_scan_varlen",
                   "ssd_state_update_slots", "ssd_state_update_multi", "ssd_conv1d_update_multi",
@@ -1039,6 +1060,271 @@ def ssd_conv1d_update_accept(xbc, conv_state, accept_len, slot_idx=None, nheads=
     _check(_lib().ssd_conv1d_update_accept(ctypes.byref(d), _ptr(xbc), CD if k == 0 else xbc.stride(1), _ptr(st),
                                            _ptr(tab), nslots, _ptr(_table(accept_len, Bt, "accept_len")),
                                            _stream(stream)), "ssd_conv1d_update_accept")
+
+
+# --------------------------------------------------------------------------- per-channel selective scan
+class _On:
+    """Makes the tensors' device, and a given stream, current for the allocations and launches of one call.
+    The buffers that the call allocates then belong to the stream that uses them."""
+
+    def __init__(self, dev, stream):
+        self.inner = []
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+            if stream != torch.cuda.current_stream(dev):
+                self.inner.append(torch.cuda.stream(stream))
+        elif dev.type == "cuda" and dev.index != torch.cuda.current_device():
+            self.inner.append(torch.cuda.device(dev))
+
+    def __enter__(self):
+        for c in self.inner:
+            c.__enter__()
+
+    def __exit__(self, *e):
+        for c in reversed(self.inner):
+            c.__exit__(*e)
+
+
+def _workspace(size, workspace, dev):
+    """(workspace tensor or None, its bytes): the caller's, or one allocated to the size the call needs."""
+    if workspace is None:
+        if size == 0:
+            return None, 0
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", dev)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _new(t, name, dev, shape, dtype):
+    """The caller's output t, checked, or a new tensor."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    return _need(t, name, dev, shape, dtype)
+
+
+def _selective_args(x, dt, A, B, C, D, z, dt_bias, rows):
+    """Checks the inputs that every per-channel call has, x with `rows` leading axes (2: [B, L, D],
+    1: [B, D]); returns (device, D, G, N, strides of x, of B and C, of z)."""
+    dev = _device(x, "x")
+    if x.dim() != rows + 1:
+        raise ValueError(f"x must have {rows + 1} axes")
+    lead, Dc = tuple(x.shape[:-1]), x.shape[-1]
+    if x.dtype not in _DT:
+        raise ValueError(f"activations must be float32 or bfloat16 (got {x.dtype})")
+    L = lead[1] if rows == 2 else 1
+    empty = x.numel() == 0
+    for t, nm in ((x, "x"), (z, "z")):
+        if t is None:
+            continue
+        _need(t, nm, dev, lead + (Dc,), x.dtype, contiguous=False)
+        if not empty and ((t.stride(-1) != 1 and Dc > 1) or (L > 1 and not _uniform_rows(t, L))):
+            raise ValueError(f"{nm} must have packed channels and a uniform token stride")
+    _need(A, "A", dev, dtype=torch.float32)
+    if A.dim() != 2 or A.shape[0] != Dc:
+        raise ValueError(f"A must be [{Dc}, N]")
+    N = A.shape[1]
+    _need(B, "B", dev, dtype=x.dtype, contiguous=False)
+    if B.dim() != rows + 2 or tuple(B.shape[:-2]) != lead or B.shape[-1] != N:
+        raise ValueError(f"B must have shape {lead + ('G', N)} (got {tuple(B.shape)})")
+    G = B.shape[-2]
+    if G == 0 or Dc % G:
+        raise ValueError(f"the channels ({Dc}) must be a multiple of B's groups ({G})")
+    _need(C, "C", dev, tuple(B.shape), x.dtype, contiguous=False)
+    for t, nm in ((B, "B"), (C, "C")):
+        if not empty and (t.stride(-1) != 1 or (G > 1 and t.stride(-2) != N) or (L > 1 and not _uniform_rows(t, L))):
+            raise ValueError(f"{nm} must have packed (G, N) and a uniform token stride")
+    one = rows == 2 and lead[0] * L <= 1 or rows == 1 and lead[0] <= 1      # one row: its stride does not matter
+    tok = rows - 1 if rows == 1 or L > 1 else 0                             # the axis whose stride parts rows
+    if not empty and not one and B.stride(tok) != C.stride(tok):
+        raise ValueError("B and C must share a token stride")
+    _need(dt, "dt", dev, lead + (Dc,), x.dtype)
+    _need(D, "D", dev, (Dc,), torch.float32, optional=True)
+    _need(dt_bias, "dt_bias", dev, (Dc,), torch.float32, optional=True)
+
+    def stride(t, least):
+        return least if t is None or empty or one else t.stride(tok)
+
+    return dev, Dc, G, N, stride(x, Dc), stride(B, G * N), stride(z, Dc)
+
+
+def ssd_selective_scan(x, dt, A, B, C, D=None, z=None, init_state=None, final_state=None, y=None, y_dtype=None,
+                       workspace=None, stream=None, dt_bias=None, dt_softplus=False, dt_limit=None):
+    """The selective scan with a decay row per channel.  x [B, L, D] and the gate z [B, L, D]|None (token
+    rows may be strided, e.g. views into projections), dt [B, L, D], A [D, N] fp32, B/C [B, L, G, N] (token
+    rows may be strided by a multiple of 16 bytes), skip weights D [D] fp32|None, init_state/final_state
+    [B, D, N] fp32|None (may be the same tensor).  dt_bias, dt_softplus and dt_limit as ssd_chunk_scan.
+    N 16, 32, 64 or 128.  Returns y [B, L, D] in y_dtype (default x's)."""
+    dev, Dc, G, N, xs, bcs, zs = _selective_args(x, dt, A, B, C, D, z, dt_bias, 2)
+    Bt, L = x.shape[:2]
+    _need(init_state, "init_state", dev, (Bt, Dc, N), torch.float32, optional=True)
+    _need(final_state, "final_state", dev, (Bt, Dc, N), torch.float32, optional=True)
+    with _On(dev, stream):
+        ydt = y_dtype or (x.dtype if y is None else y.dtype)
+        y = _new(y, "y", dev, (Bt, L, Dc), ydt)
+        d = _dims(Bt, L, Dc, 1, G, N, x.dtype, ydt)
+        workspace, ws = _workspace(int(_lib().ssd_selective_scan_workspace_size(ctypes.byref(d))), workspace, dev)
+        _check(_lib().ssd_selective_scan(ctypes.byref(d), _ptr(x), xs, _ptr(dt), _ptr(A), _ptr(B), _ptr(C), bcs, _ptr(D),
+                                         _ptr(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit), _ptr(init_state),
+                                         _ptr(final_state), _ptr(y), _ptr(workspace), ws, _stream(stream)),
+               "ssd_selective_scan")
+    return y
+
+
+def ssd_selective_scan_bwd(dy, x, dt, A, B, C, D=None, z=None, init_state=None, dfinal_state=None, workspace=None,
+                           stream=None, dt_bias=None, dt_softplus=False, dt_limit=None):
+    """Gradients of ssd_selective_scan from its inputs, dy [B, L, D] (contiguous, in y's dtype) and
+    dfinal_state [B, D, N] fp32|None.  Returns a dict: dx, ddt, dz [B, L, D] and dB, dC [B, L, G, N] in x's
+    dtype, dA [D, N], dD [D], ddt_bias [D] and dinit_state [B, D, N] in fp32; None where the input is
+    None."""
+    dev, Dc, G, N, xs, bcs, zs = _selective_args(x, dt, A, B, C, D, z, dt_bias, 2)
+    Bt, L = x.shape[:2]
+    _need(dy, "dy", dev, (Bt, L, Dc))
+    _need(init_state, "init_state", dev, (Bt, Dc, N), torch.float32, optional=True)
+    _need(dfinal_state, "dfinal_state", dev, (Bt, Dc, N), torch.float32, optional=True)
+    d = _dims(Bt, L, Dc, 1, G, N, x.dtype, dy.dtype)
+    with _On(dev, stream):
+        def new(like, shape, dtype):
+            return None if like is None else torch.empty(shape, dtype=dtype, device=dev)
+
+        o = {"dx": new(x, x.shape, x.dtype), "ddt": new(x, x.shape, x.dtype), "dA": new(A, A.shape, A.dtype),
+             "dB": new(B, B.shape, x.dtype), "dC": new(C, C.shape, x.dtype), "dD": new(D, (Dc,), torch.float32),
+             "dz": new(z, x.shape, x.dtype), "ddt_bias": new(dt_bias, (Dc,), torch.float32),
+             "dinit_state": new(init_state, (Bt, Dc, N), torch.float32)}
+        workspace, ws = _workspace(int(_lib().ssd_selective_scan_bwd_workspace_size(ctypes.byref(d))), workspace, dev)
+        _check(_lib().ssd_selective_scan_bwd(ctypes.byref(d), _ptr(dy), _ptr(x), xs, _ptr(dt), _ptr(A), _ptr(B), _ptr(C),
+                                             bcs, _ptr(D), _ptr(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
+                                             _ptr(init_state), _ptr(dfinal_state), _ptr(o["dx"]), _ptr(o["ddt"]),
+                                             _ptr(o["dA"]), _ptr(o["dB"]), _ptr(o["dC"]), _ptr(o["dD"]), _ptr(o["dz"]),
+                                             _ptr(o["ddt_bias"]), _ptr(o["dinit_state"]), _ptr(workspace), ws,
+                                             _stream(stream)), "ssd_selective_scan_bwd")
+    return o
+
+
+def ssd_selective_state_update(state, x, dt, A, B, C, D=None, z=None, slot_idx=None, state_out=None, y=None,
+                               y_dtype=None, stream=None, dt_bias=None, dt_softplus=False, dt_limit=None):
+    """One token of the per-channel scan.  state [B, D, N] fp32, or with slot_idx [B] int32 a pool
+    [nslots, D, N]; updated in place, or with state_out (same shape, other memory) read there and written
+    here, the named entries alone.  x, z [B, D] and B/C [B, G, N] (rows may be strided), dt [B, D].
+    Returns y [B, D]."""
+    dev, Dc, G, N, xs, bcs, zs = _selective_args(x, dt, A, B, C, D, z, dt_bias, 1)
+    Bt = x.shape[0]
+    _need(state, "state", dev, dtype=torch.float32)
+    if state.dim() != 3 or tuple(state.shape[1:]) != (Dc, N):
+        raise ValueError(f"state must be [B or nslots, {Dc}, {N}]")
+    _need(state_out, "state_out", dev, tuple(state.shape), torch.float32, optional=True)
+    _need(slot_idx, "slot_idx", dev, optional=True)
+    if state_out is not None and state_out.data_ptr() != state.data_ptr() and state.numel() > 0 and \
+            abs(state_out.data_ptr() - state.data_ptr()) < 4 * state.numel():
+        raise ValueError("state_out must be state or not overlap it")
+    st, nslots, tab = _state_pool_args(state, slot_idx, Bt)
+    with _On(dev, stream):
+        ydt = y_dtype or (x.dtype if y is None else y.dtype)
+        y = _new(y, "y", dev, (Bt, Dc), ydt)
+        d = _dims(Bt, 1, Dc, 1, G, N, x.dtype, ydt)
+        _check(_lib().ssd_selective_state_update(ctypes.byref(d), _ptr(st), _ptr(st if state_out is None else state_out),
+                                                 _ptr(tab), nslots, _ptr(x), xs, _ptr(dt), _ptr(A), _ptr(B), _ptr(C), bcs,
+                                                 _ptr(D), _ptr(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
+                                                 _ptr(y), _stream(stream)), "ssd_selective_state_update")
+    return y
+
+
+def ssd_conv1d_bwd(dout, xbc, w, bias=None, conv_state_in=None, dconv_state_out=None, nheads=None, head_dim=None,
+                   ngroups=None, d_state=None, workspace=None, stream=None):
+    """Gradients of ssd_conv1d_fwd from its inputs, dout [B, L, CD] (contiguous) and dconv_state_out
+    [B, CD, 4]|None.  Returns a dict: dxbc [B, L, CD] and dconv_state_in [B, CD, 4] in xbc's dtype, dw
+    [CD, 4] and dbias [CD] in fp32; None where the input is None."""
+    dev = _device(xbc, "xbc")
+    if xbc.dim() != 3:
+        raise ValueError("xbc must be [B, L, CD]")
+    Bt, L, CD = xbc.shape
+    if L > 0 and ((xbc.stride(2) != 1 and CD > 1) or (L > 1 and not _uniform_rows(xbc, L))):
+        raise ValueError("xbc must be [B, L, CD] with packed channels and uniform token stride")
+    H, P, G, N = _split_cd(CD, nheads, head_dim, ngroups, d_state)
+    _conv_params(dev, CD, xbc.dtype, w, bias)
+    _need(dout, "dout", dev, (Bt, L, CD), xbc.dtype)
+    _need(conv_state_in, "conv_state_in", dev, (Bt, CD, 4), xbc.dtype, optional=True)
+    _need(dconv_state_out, "dconv_state_out", dev, (Bt, CD, 4), xbc.dtype, optional=True)
+    d = _dims(Bt, L, H, P, G, N, xbc.dtype, xbc.dtype)
+    xs = CD if Bt * L <= 1 else xbc.stride(1) if L > 1 else xbc.stride(0)
+    with _On(dev, stream):
+        def new(like, shape, dtype):
+            return None if like is None else torch.empty(shape, dtype=dtype, device=dev)
+
+        o = {"dxbc": new(xbc, (Bt, L, CD), xbc.dtype), "dw": new(w, (CD, 4), torch.float32),
+             "dbias": new(bias, (CD,), torch.float32), "dconv_state_in": new(conv_state_in, (Bt, CD, 4), xbc.dtype)}
+        workspace, ws = _workspace(int(_lib().ssd_conv1d_bwd_workspace_size(ctypes.byref(d))), workspace, dev)
+        _check(_lib().ssd_conv1d_bwd(ctypes.byref(d), _ptr(xbc), xs, _ptr(w), _ptr(bias), _ptr(conv_state_in), _ptr(dout),
+                                     _ptr(dconv_state_out), _ptr(o["dxbc"]), _ptr(o["dw"]), _ptr(o["dbias"]),
+                                     _ptr(o["dconv_state_in"]), _ptr(workspace), ws, _stream(stream)), "ssd_conv1d_bwd")
+    return o
+
+
+# --------------------------------------------------------------------------- slots of state pools
+def _pool(pool, name, dev, stacked):
+    """(slots, bytes of a slot, layers, layer stride) of pool [nslots, ...], or [layers, nslots, ...]."""
+    _need(pool, name, dev)
+    lead = 2 if stacked else 1
+    if pool.dim() < lead:
+        raise ValueError(f"{name} must be [{'layers, ' if stacked else ''}nslots, ...]")
+    layers = pool.shape[0] if stacked else 1
+    nslots = pool.shape[lead - 1]
+    slot = pool.element_size()
+    for n in pool.shape[lead:]:
+        slot *= n
+    return nslots, slot, layers, nslots * slot
+
+
+def ssd_pool_copy(dst_pool, dst_idx, src_pool, src_idx, stacked=False, stream=None):
+    """dst_pool[dst_idx[i]] = src_pool[src_idx[i]] for each i in turn, on the device, in place: forks (one
+    source for several destinations), prefixes saved to or restored from a snapshot pool, a compaction's
+    moves.  Pools [nslots, ...] of one slot shape and dtype, or [layers, nslots, ...] with stacked (every
+    layer is copied alike); the two may be one tensor.  dst_idx, src_idx [n] int32; an entry with an
+    index that names no slot is skipped."""
+    dev = _device(dst_pool, "dst_pool")
+    dn, slot, layers, dls = _pool(dst_pool, "dst_pool", dev, stacked)
+    sn, sslot, slayers, sls = _pool(src_pool, "src_pool", dev, stacked)
+    lead = 2 if stacked else 1
+    if dst_pool.dtype != src_pool.dtype or dst_pool.shape[lead:] != src_pool.shape[lead:] or layers != slayers:
+        raise ValueError("both pools must have the same dtype, slot shape and layers")
+    _need(dst_idx, "dst_idx", dev)
+    _need(src_idx, "src_idx", dev)
+    n = dst_idx.numel()
+    with _On(dev, stream):
+        _check(_lib().ssd_pool_copy(_ptr(dst_pool), dn, dls, _ptr(src_pool), sn, sls, slot, layers,
+                                    _ptr(_table(dst_idx, n, "dst_idx")), _ptr(_table(src_idx, n, "src_idx")), n,
+                                    _stream(stream)), "ssd_pool_copy")
+    return dst_pool
+
+
+def ssd_pool_clear(pool, slot_idx, stacked=False, stream=None):
+    """Zeroes the slots slot_idx [n] int32 of pool [nslots, ...] (or of every layer of [layers, nslots, ...]
+    with stacked), in place; indices that name no slot are skipped."""
+    dev = _device(pool, "pool")
+    nslots, slot, layers, ls = _pool(pool, "pool", dev, stacked)
+    _need(slot_idx, "slot_idx", dev)
+    n = slot_idx.numel()
+    with _On(dev, stream):
+        _check(_lib().ssd_pool_clear(_ptr(pool), nslots, ls, slot, layers, _ptr(_table(slot_idx, n, "slot_idx")), n,
+                                     _stream(stream)), "ssd_pool_clear")
+    return pool
+
+
+def ssd_pool_compact(slot_idx, nslots, stream=None):
+    """The plan that moves the live slots slot_idx [n] int32 (repeats and padding allowed) to the front of a
+    pool of nslots <= 131072.  Returns (src_idx [n], dst_idx [n], new_slot_idx [n], count []) int32 on the
+    device: ssd_pool_copy(pool, dst_idx, pool, src_idx) makes the moves in each pool that the table serves,
+    new_slot_idx replaces the table, and slots from count on are free."""
+    dev = _device(slot_idx, "slot_idx")
+    _need(slot_idx, "slot_idx", dev)
+    n = slot_idx.numel()
+    _table(slot_idx, n, "slot_idx")
+    with _On(dev, stream):
+        out = torch.empty((3, n), dtype=torch.int32, device=dev)
+        count = torch.empty((), dtype=torch.int32, device=dev)
+        _check(_lib().ssd_pool_compact(_ptr(slot_idx), n, int(nslots), _ptr(out[0]), _ptr(out[1]), _ptr(out[2]),
+                                       _ptr(count), _stream(stream)), "ssd_pool_compact")
+    return out[0], out[1], out[2], count
 
 
 def split_xbc(v, nheads, head_dim, ngroups, d_state):
