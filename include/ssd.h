@@ -571,7 +571,7 @@ ssd_status_t ssd_conv1d_update_accept(const ssd_dims_t* d, const void* xbc, int6
 /*
  * Scan of a prefill.
  *  x, z         [B, L, D] act dtype; token rows x_row_stride / z_row_stride elements apart (>= D),
- *               batch rows L rows apart.  x may be the conv's output, z a view into in_proj's.  z may
+ *               batch rows L rows apart; D and row strides are at most 2^24.  x may be the conv's output, z a view into in_proj's.  z may
  *               be NULL (no gate; its stride is then not read).
  *  dt           [B, L, D] contiguous act dtype.  dt_params as for ssd_chunk_scan, bias [D].
  *  A            [D, N] fp32.  Dskip: [D] fp32 or NULL.

@@ -20,37 +20,62 @@ __device__ __forceinline__ float sel_softplus(float v) {
     const float l = u == 1.f ? e : e * (__builtin_amdgcn_logf(u) * 0.69314718055994530942f) * __builtin_amdgcn_rcpf(u - 1.f);
     return v > 20.f ? v : l;
 }
+template <int K>
+__device__ __forceinline__ void sel_dts(float (&v)[K], const SelDt& p) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] += p.bias;
+    if (p.softplus)
+#pragma unroll
+        for (int i = 0; i < K; ++i) v[i] = sel_softplus(v[i]);
+    if (p.lo < p.hi)
+#pragma unroll
+        for (int i = 0; i < K; ++i) v[i] = fminf(fmaxf(v[i], p.lo), p.hi);
+}
 __device__ __forceinline__ float sel_dt(float v, const SelDt& p) {
-    v += p.bias;
-    if (p.softplus) v = sel_softplus(v);
-    if (p.lo < p.hi) v = fminf(fmaxf(v, p.lo), p.hi);
-    return v;
+    float a[1] = {v};
+    sel_dts(a, p);
+    return a[0];
 }
 
-// S consecutive values of a row that every lane of the wave reads: scalar loads (the row is 16-byte
-// aligned and S >= 4), widened by scalar shifts.
+// B and C of n consecutive tokens, S consecutive states of each: rows that every lane of a wave reads
+// alike.  They are held as loaded, in scalar registers (16 of them where S allows it), and widened by
+// scalar shifts.  Rows are 16-byte aligned, `stride` bytes apart; none past row `last` is read (the
+// last one repeats).
 typedef const uint32_t __attribute__((address_space(4))) ScalarWord;
+typedef const char __attribute__((address_space(4))) ScalarByte;
 template <typename T, int S>
-__device__ __forceinline__ void load_uniform(const T* p, float (&o)[S]) {
-    ScalarWord* q = (ScalarWord*)(uintptr_t)p;
-    if constexpr (Vec16<T>::n == 8) {
+struct SelRows {
+    static constexpr int kWords = S * static_cast<int>(sizeof(T)) / 4;   // of one row
+    static constexpr int n = kWords >= 8 ? 1 : 8 / kWords;
+    uint32_t bw[n][kWords], cw[n][kWords];
+    template <bool WITH_C>
+    __device__ __forceinline__ void load(const char* b, const char* c, uint32_t stride, int first, int last) {
 #pragma unroll
-        for (int i = 0; i < S / 2; ++i) {
-            const uint32_t v = q[i];
-            o[2 * i] = __uint_as_float(v << 16);
-            o[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
+        for (int t = 0; t < n; ++t) {
+            const uint32_t o = static_cast<uint32_t>(first + t < last ? first + t : last) * stride;
+            ScalarWord* p = (ScalarWord*)((ScalarByte*)(uintptr_t)b + o);
+            ScalarWord* q = (ScalarWord*)((ScalarByte*)(uintptr_t)c + o);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) bw[t][i] = p[i];
+            if constexpr (WITH_C)
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) cw[t][i] = q[i];
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < S; ++i) o[i] = __uint_as_float(q[i]);
     }
-}
+    static __device__ __forceinline__ float value(const uint32_t* w, int s) {
+        if constexpr (sizeof(T) == 2) return __uint_as_float(s & 1 ? w[s / 2] & 0xffff0000u : w[s / 2] << 16);
+        else return __uint_as_float(w[s]);
+    }
+    __device__ __forceinline__ float b(int t, int s) const { return value(bw[t], s); }
+    __device__ __forceinline__ float c(int t, int s) const { return value(cw[t], s); }
+};
 
 // Which channels, and which batch entry, a workgroup has: 64-channel blocks never straddle groups.
 struct SelBlock {
     int64_t b;
     int blk, g, c0, cend;
 };
+__host__ __device__ __forceinline__ int64_t sel_blocks(int D, int G) { return static_cast<int64_t>(G) * ((D / G + 63) / 64); }
 __device__ __forceinline__ SelBlock sel_block(int64_t id, int D, int G) {
     const int cpg = D / G, per = (cpg + 63) / 64, nblk = per * G;
     SelBlock r;

@@ -18,24 +18,47 @@ namespace ssd {
 
 constexpr int kSelTile = 16;   // tokens staged at a time
 
-template <typename T, typename TY, int S, int W>
-__global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a) {
+// Sequences are cut into chunks of `tokens` when there are too few workgroups otherwise (sel_chunks).
+// Then a first launch (Y false) runs each chunk but the last from a zero state and leaves its final
+// state [B][chunks][N][D] and its sum of dt [B][chunks][D]; a chunk's state at its first token follows from
+// those of the chunks before it, since a chunk multiplies the state it starts from by exp(A sum dt).
+struct SelChunks {
+    int64_t tokens;
+    int n;
+    float* ends;
+    float* sums;
+};
+
+template <typename T, typename TY, int S, int W, bool Y, bool GATE>
+__global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, SelChunks ch) {
     constexpr int N = S * W, TPT = kSelTile / W;   // tokens of a tile that one thread stages
+    constexpr int SUB = SelRows<T, S>::n;          // tokens whose B and C are in scalar registers
+    constexpr int E = sizeof(T);
     __shared__ float2 st[2][kSelTile][64];         // dt, dt * x
-    __shared__ float part[2][W][kSelTile][64];
-    const SelBlock k = sel_block(blockIdx.x, a.channels, a.ngroups);
+    __shared__ float part[Y ? 2 : 1][Y ? W : 1][kSelTile][64];
+    const int64_t per_chunk = a.batch * sel_blocks(a.channels, a.ngroups);
+    const int chunk = static_cast<int>(blockIdx.x / per_chunk);
+    const SelBlock k = sel_block(blockIdx.x % per_chunk, a.channels, a.ngroups);
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = k.c0 + lane;
     const bool ok = c < k.cend;
     const int cs = ok ? c : k.c0;                  // lanes past the group read its first channel, store nothing
-    const int64_t L = a.seqlen, D = a.channels;
-    const T* xp = static_cast<const T*>(a.x) + k.b * L * a.x_row_stride + cs;
-    const T* zp = a.z ? static_cast<const T*>(a.z) + k.b * L * a.z_row_stride + cs : nullptr;
-    const T* dp = static_cast<const T*>(a.dt) + k.b * L * D + cs;
-    const T* Bp = static_cast<const T*>(a.B) + k.b * L * a.bc_row_stride + k.g * N + w * S;
-    const T* Cp = static_cast<const T*>(a.C) + k.b * L * a.bc_row_stride + k.g * N + w * S;
-    TY* yp = static_cast<TY*>(a.y) + k.b * L * D + cs;
+    const int64_t D = a.channels;
+    const int64_t r0 = k.b * a.seqlen + chunk * ch.tokens;   // first token row
+    const int64_t left = a.seqlen - chunk * ch.tokens;
+    const int L = static_cast<int>(left < ch.tokens ? left : ch.tokens);   // the chunk's tokens
+    // per stream: the tile's first row (scalar, advanced tile by tile), and offsets in bytes from there
+    // (16 rows and a bit, in 32 bits: row strides are at most 2^24 elements)
+    const char* xp = static_cast<const char*>(a.x) + (r0 * a.x_row_stride + k.c0) * E;
+    const char* zp = GATE ? static_cast<const char*>(a.z) + (r0 * a.z_row_stride + k.c0) * E : nullptr;
+    const char* dp = static_cast<const char*>(a.dt) + (r0 * D + k.c0) * E;
+    const char* Bp = static_cast<const char*>(a.B) + (r0 * a.bc_row_stride + k.g * N + w * S) * E;
+    const char* Cp = static_cast<const char*>(a.C) + (r0 * a.bc_row_stride + k.g * N + w * S) * E;
+    char* yp = static_cast<char*>(a.y) + (r0 * D + k.c0) * sizeof(TY);
+    const uint32_t xs = static_cast<uint32_t>(a.x_row_stride) * E, zs = static_cast<uint32_t>(a.z_row_stride) * E;
+    const uint32_t ds = static_cast<uint32_t>(D) * E, ys = static_cast<uint32_t>(D) * sizeof(TY), bs = static_cast<uint32_t>(a.bc_row_stride) * E;
+    const uint32_t le = (cs - k.c0) * E;
     const SelDt dtp{a.dtp.bias ? a.dtp.bias[cs] : 0.f, a.dtp.lo, a.dtp.hi, a.dtp.softplus};
     const float Dv = a.D ? a.D[cs] : 0.f;
     float A2[S], h[S];
@@ -43,88 +66,199 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a) {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         A2[s] = a.A[static_cast<int64_t>(cs) * N + w * S + s] * kLog2e;
-        h[s] = a.init_state ? a.init_state[so + s] : 0.f;
+        h[s] = Y && a.init_state ? a.init_state[so + s] : 0.f;
     }
-    float xr[TPT], zr[TPT], dr[TPT];
-    auto load = [&](int64_t t0) {
+    if constexpr (Y)
+        for (int p = 0; p < chunk; ++p) {
+            const float sum = ch.sums[(k.b * ch.n + p) * D + cs];
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                h[s] = fmaf(__builtin_amdgcn_exp2f(sum * A2[s]), h[s], ch.ends[((k.b * ch.n + p) * N + w * S + s) * D + cs]);
+        }
+    T xr[TPT], zr[TPT], dr[TPT];     // the next tile's values as loaded
+    float xk[TPT], zk[TPT], sum = 0.f;
+    uint32_t ahead = 0;
+    // this thread's tokens first + w + W i of the tile, none past row `last`
+    auto load = [&](int first, int last) {
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
-            const int64_t t = t0 + w + W * i;
-            const bool in = t < L;
-            const int64_t tt = in ? t : L - 1;
-            xr[i] = static_cast<float>(xp[tt * a.x_row_stride]);
-            dr[i] = static_cast<float>(dp[tt * D]);
-            zr[i] = zp ? static_cast<float>(zp[tt * a.z_row_stride]) : 0.f;
+            const uint32_t t = static_cast<uint32_t>(first + w + W * i < last ? first + w + W * i : last);
+            xr[i] = *reinterpret_cast<const T*>(xp + static_cast<uint64_t>(t * xs) + le);
+            dr[i] = *reinterpret_cast<const T*>(dp + static_cast<uint64_t>(t * ds) + le);
+            if constexpr (GATE) zr[i] = *reinterpret_cast<const T*>(zp + static_cast<uint64_t>(t * zs) + le);
+        }
+        // B and C of the tile, a token a lane: brings the rows, which each wave reads through the scalar
+        // cache a few tokens before it needs them, near in time
+        const uint32_t t = static_cast<uint32_t>(first + (lane & 15) < last ? first + (lane & 15) : last);
+        ahead = *reinterpret_cast<const uint32_t*>((lane & 16 ? Cp : Bp) + static_cast<uint64_t>(t * bs));
+    };
+    // y of the tile before the one that starts at yp, whose partial sums lie in part[buf]; rows past
+    // `last` of it do not exist
+    auto finish = [&](int buf, int last) {
+        if constexpr (Y) {
+            float y[TPT];
+#pragma unroll
+            for (int i = 0; i < TPT; ++i) {
+                y[i] = Dv * xk[i];
+#pragma unroll
+                for (int v = 0; v < W; ++v) y[i] += part[buf][v][w + W * i][lane];
+                if constexpr (GATE) y[i] *= silu_f(zk[i]);
+            }
+            char* base = yp - static_cast<int64_t>(kSelTile) * ys;
+            auto store = [&](int i) {
+                *reinterpret_cast<TY*>(base + static_cast<uint64_t>(static_cast<uint32_t>(w + W * i) * ys) + lane * sizeof(TY)) = static_cast<TY>(y[i]);
+            };
+            if (ok && last >= kSelTile - 1) {
+#pragma unroll
+                for (int i = 0; i < TPT; ++i) store(i);
+            } else if (ok) {
+#pragma unroll
+                for (int i = 0; i < TPT; ++i)
+                    if (w + W * i <= last) store(i);
+            }
         }
     };
-    if (L > 0) load(0);
-    int buf = 0;
-    for (int64_t t0 = 0; t0 < L; t0 += kSelTile, buf ^= 1) {
-        float xk[TPT], zk[TPT];
-#pragma unroll
-        for (int i = 0; i < TPT; ++i) {
-            const int t = w + W * i;
-            const float dt = t0 + t < L ? sel_dt(dr[i], dtp) : 0.f;   // past the end: the state stands still
-            const float x = t0 + t < L ? xr[i] : 0.f;
-            st[buf][t][lane] = make_float2(dt, dt * x);
-            xk[i] = x;
-            zk[i] = zr[i];
-        }
-        __syncthreads();
-        if (t0 + kSelTile < L) load(t0 + kSelTile);
-#pragma unroll 4
-        for (int t = 0; t < kSelTile; ++t) {
-            const int64_t row = t0 + t < L ? t0 + t : L - 1;
-            float Bv[S], Cv[S];
-            load_uniform<T, S>(Bp + row * a.bc_row_stride, Bv);
-            load_uniform<T, S>(Cp + row * a.bc_row_stride, Cv);
-            const float2 d = st[buf][t][lane];
-            float y = 0.f;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const float e = __builtin_amdgcn_exp2f(d.x * A2[s]);
-                h[s] = fmaf(e, h[s], d.y * Bv[s]);
-                y = fmaf(h[s], Cv[s], y);
-            }
-            part[buf][w][t][lane] = y;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < TPT; ++i) {
-            const int t = w + W * i;
-            float y = Dv * xk[i];
-#pragma unroll
-            for (int v = 0; v < W; ++v) y += part[buf][v][t][lane];
-            if (zp) y *= silu_f(zk[i]);
-            if (ok && t0 + t < L) yp[(t0 + t) * D] = static_cast<TY>(y);
-        }
+    SelRows<T, S> rows[2];
+    float2 d[2][SUB];
+    if (L > 0) {
+        load(0, L - 1);
+        rows[0].template load<Y>(Bp, Cp, bs, 0, L - 1);
     }
-    if (a.final_state && ok) {
+    int buf = 0;
+    for (int t0 = 0; t0 < L; t0 += kSelTile, buf ^= 1) {
+        const int last = L - 1 - t0;
+        float xn[TPT], dn[TPT], zn[TPT];
 #pragma unroll
-        for (int s = 0; s < S; ++s) a.final_state[so + s] = h[s];
+        for (int i = 0; i < TPT; ++i) {
+            xn[i] = static_cast<float>(xr[i]);
+            dn[i] = static_cast<float>(dr[i]);
+            if constexpr (GATE) zn[i] = static_cast<float>(zr[i]);
+        }
+        asm volatile("" ::"v"(ahead));
+        sel_dts(dn, dtp);
+        if (last < kSelTile - 1)                              // past the end the state stands still
+#pragma unroll
+            for (int i = 0; i < TPT; ++i)
+                if (w + W * i > last) xn[i] = dn[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+            st[buf][w + W * i][lane] = make_float2(dn[i], dn[i] * xn[i]);
+            if constexpr (!Y) sum += dn[i];
+        }
+        __syncthreads();
+        load(kSelTile, last);
+#pragma unroll
+        for (int t = 0; t < SUB; ++t) d[0][t] = st[buf][t][lane];
+        if (t0 > 0) finish(buf ^ 1, kSelTile);
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+            xk[i] = xn[i];
+            if constexpr (GATE) zk[i] = zn[i];
+        }
+#pragma unroll
+        for (int u = 0; u < kSelTile; u += SUB) {
+            const int at = (u / SUB) & 1;
+            // the next tokens' B, C, dt and dt * x are fetched while these are used
+            rows[at ^ 1].template load<Y>(Bp, Cp, bs, u + SUB, last);
+            if (u + SUB < kSelTile)
+#pragma unroll
+                for (int t = 0; t < SUB; ++t) d[at ^ 1][t] = st[buf][u + SUB + t][lane];
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = 0; t < SUB; ++t) {
+                float y = 0.f;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const float e = __builtin_amdgcn_exp2f(d[at][t].x * A2[s]);
+                    h[s] = fmaf(e, h[s], d[at][t].y * rows[at].b(t, s));
+                    if constexpr (Y) y = fmaf(h[s], rows[at].c(t, s), y);
+                }
+                if constexpr (Y) part[buf][w][u + t][lane] = y;
+            }
+        }
+        xp += static_cast<int64_t>(kSelTile) * xs;
+        dp += static_cast<int64_t>(kSelTile) * ds;
+        if constexpr (GATE) zp += static_cast<int64_t>(kSelTile) * zs;
+        Bp += static_cast<int64_t>(kSelTile) * bs;
+        Cp += static_cast<int64_t>(kSelTile) * bs;
+        yp += static_cast<int64_t>(kSelTile) * ys;
+    }
+    __syncthreads();
+    if constexpr (Y) {
+        if (L > 0) finish(buf ^ 1, (L - 1) % kSelTile);
+        if (a.final_state && ok && chunk == ch.n - 1) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) a.final_state[so + s] = h[s];
+        }
+    } else {
+        st[0][w][lane] = make_float2(sum, 0.f);
+        __syncthreads();
+        if (ok) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) ch.ends[((k.b * ch.n + chunk) * N + w * S + s) * D + c] = h[s];
+            if (w == 0) {
+                float v = 0.f;
+#pragma unroll
+                for (int i = 0; i < W; ++i) v += st[0][i][lane].x;
+                ch.sums[(k.b * ch.n + chunk) * D + c] = v;
+            }
+        }
     }
 }
 
-template <typename T, typename TY>
-static hipError_t scan_t(const SelScanArgs& a, hipStream_t s) {
-    const int64_t blocks = a.batch * a.ngroups * ((a.channels / a.ngroups + 63) / 64);
-    const dim3 grid(static_cast<uint32_t>(blocks));
-    switch (a.d_state) {
-        case 16: hipLaunchKernelGGL((selective_scan_kernel<T, TY, 4, 4>), grid, dim3(256), 0, s, a); break;
-        case 32: hipLaunchKernelGGL((selective_scan_kernel<T, TY, 8, 4>), grid, dim3(256), 0, s, a); break;
-        case 64: hipLaunchKernelGGL((selective_scan_kernel<T, TY, 16, 4>), grid, dim3(256), 0, s, a); break;
-        case 128: hipLaunchKernelGGL((selective_scan_kernel<T, TY, 16, 8>), grid, dim3(512), 0, s, a); break;
-        default: return hipErrorInvalidValue;
-    }
+constexpr int sel_waves(int d_state) { return d_state == 128 ? 8 : 4; }
+
+// Chunks of a sequence.  The kernel wants three waves or more on each of the 1024 SIMDs; below 1024 waves
+// in all, the second pass that chunks cost (5/6 of the first one's vector operations) is less than what
+// stands idle.  Measured, 16 states, bf16: 2 x 8192 tokens x 4096 channels (512 waves) 1108 us in one
+// chunk, 616 with 2048 waves, 552 with 3072, 529 with 8192; 1 x 2048 x 4096 277, 84, 79, 83; 8 x 2048 x
+// 4096 (2048 waves) 344 in one chunk, 438 in two.
+static SelChunks sel_chunks(int64_t batch, int64_t L, int channels, int ngroups, int d_state) {
+    const int64_t waves = batch * sel_blocks(channels, ngroups) * sel_waves(d_state);
+    int64_t n = waves >= 1024 || waves == 0 ? 1 : (6144 + waves - 1) / waves;
+    if (n > L / 64) n = L / 64 > 0 ? L / 64 : 1;   // a chunk has 64 tokens or more
+    int64_t tokens = (L + n - 1) / n;
+    tokens = (tokens + kSelTile - 1) / kSelTile * kSelTile;
+    if (n == 1) tokens = L > 0 ? L : 1;
+    SelChunks c{tokens, static_cast<int>(L > 0 ? (L + tokens - 1) / tokens : 1), nullptr, nullptr};
+    return c;
+}
+
+template <typename T, typename TY, int S, int W>
+static hipError_t scan_launch(const SelScanArgs& a, const SelChunks& ch, hipStream_t s) {
+    const int64_t per_chunk = a.batch * sel_blocks(a.channels, a.ngroups);
+    if (ch.n > 1)
+        hipLaunchKernelGGL((selective_scan_kernel<T, TY, S, W, false, false>), dim3(static_cast<uint32_t>(per_chunk * (ch.n - 1))),
+                           dim3(64 * W), 0, s, a, ch);
+    const dim3 grid(static_cast<uint32_t>(per_chunk * ch.n)), block(64 * W);
+    if (a.z) hipLaunchKernelGGL((selective_scan_kernel<T, TY, S, W, true, true>), grid, block, 0, s, a, ch);
+    else hipLaunchKernelGGL((selective_scan_kernel<T, TY, S, W, true, false>), grid, block, 0, s, a, ch);
     return hipGetLastError();
 }
 
-size_t selective_scan_workspace_bytes(int64_t, int64_t, int, int, int) { return 0; }
+template <typename T, typename TY>
+static hipError_t scan_t(const SelScanArgs& a, const SelChunks& ch, hipStream_t s) {
+    switch (a.d_state) {
+        case 16: return scan_launch<T, TY, 4, 4>(a, ch, s);
+        case 32: return scan_launch<T, TY, 8, 4>(a, ch, s);
+        case 64: return scan_launch<T, TY, 16, 4>(a, ch, s);
+        case 128: return scan_launch<T, TY, 16, 8>(a, ch, s);
+        default: return hipErrorInvalidValue;
+    }
+}
 
-hipError_t launch_selective_scan(const SelScanArgs& a, Dt act, Dt ydt, void*, hipStream_t s) {
+size_t selective_scan_workspace_bytes(int64_t batch, int64_t seqlen, int channels, int ngroups, int d_state) {
+    const SelChunks c = sel_chunks(batch, seqlen, channels, ngroups, d_state);
+    return c.n > 1 ? static_cast<size_t>(batch * c.n * (d_state + 1) * channels) * sizeof(float) : 0;
+}
+
+hipError_t launch_selective_scan(const SelScanArgs& a, Dt act, Dt ydt, void* workspace, hipStream_t s) {
     if (a.batch == 0) return hipSuccess;
-    if (act == Dt::BF16) return ydt == Dt::BF16 ? scan_t<bf16, bf16>(a, s) : scan_t<bf16, float>(a, s);
-    return ydt == Dt::BF16 ? scan_t<float, bf16>(a, s) : scan_t<float, float>(a, s);
+    SelChunks c = sel_chunks(a.batch, a.seqlen, a.channels, a.ngroups, a.d_state);
+    c.ends = static_cast<float*>(workspace);
+    c.sums = c.ends + a.batch * c.n * a.d_state * static_cast<int64_t>(a.channels);
+    if (act == Dt::BF16) return ydt == Dt::BF16 ? scan_t<bf16, bf16>(a, c, s) : scan_t<bf16, float>(a, c, s);
+    return ydt == Dt::BF16 ? scan_t<float, bf16>(a, c, s) : scan_t<float, float>(a, c, s);
 }
 
 // One token per batch entry.  The state is read once and written once: an HBM stream.  A thread owns

@@ -22,6 +22,22 @@
 
 namespace ssd {
 
+template <typename T, int S>
+__device__ __forceinline__ void load_uniform(const T* p, float (&o)[S]) {
+    ScalarWord* q = (ScalarWord*)(uintptr_t)p;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < S / 2; ++i) {
+            const uint32_t v = q[i];
+            o[2 * i] = __uint_as_float(v << 16);
+            o[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < S; ++i) o[i] = __uint_as_float(q[i]);
+    }
+}
+
 template <int S>
 struct SelTile {
     static constexpr int T = 64 / S;   // tokens per tile: 64 (token, state) pairs a lane

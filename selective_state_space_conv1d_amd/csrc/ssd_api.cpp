@@ -64,6 +64,11 @@ bool selective_sizes_ok(const ssd_dims_t* d, int64_t seqlen) {
     const int64_t rows = d->batch * seqlen;
     return rows == 0 || (kMax * 256LL - params) / per_row >= rows;
 }
+// Row strides (bytes of 16 rows and more in 32 bits) of the per-channel scan's streams.
+bool selective_strides_ok(const ssd_dims_t* d, int64_t xs, int64_t bcs, int64_t zs) {
+    constexpr int64_t kMax = INT64_C(1) << 24;
+    return d->nheads <= kMax && xs <= kMax && bcs <= kMax && zs <= kMax;
+}
 ssd_status_t check_workspace(const void* p, size_t have, size_t need) {
     if (need == 0) return SSD_OK;
     if (!p || have < need) return SSD_ERR_WORKSPACE;
@@ -701,6 +706,7 @@ ssd_status_t ssd_selective_scan(const ssd_dims_t* d, const void* x, int64_t x_ro
     if (!selective_sizes_ok(d, d->seqlen)) return SSD_ERR_UNSUPPORTED;
     const int64_t GN = static_cast<int64_t>(d->ngroups) * d->d_state;
     if (tokens && (x_row_stride < d->nheads || bc_row_stride < GN || (z && z_row_stride < d->nheads))) return SSD_ERR_SHAPE;
+    if (tokens && !selective_strides_ok(d, x_row_stride, bc_row_stride, z ? z_row_stride : 0)) return SSD_ERR_UNSUPPORTED;
     if (tokens && !stride_ok(bc_row_stride, d->act_dtype)) return SSD_ERR_ALIGN;
     for (const void* p : {B, C})
         if (p && !aligned16(p)) return SSD_ERR_ALIGN;
@@ -739,6 +745,7 @@ ssd_status_t ssd_selective_scan_bwd(const ssd_dims_t* d, const void* dy, const v
     if (!selective_sizes_ok(d, d->seqlen)) return SSD_ERR_UNSUPPORTED;
     const int64_t GN = static_cast<int64_t>(d->ngroups) * d->d_state;
     if (tokens && (x_row_stride < d->nheads || bc_row_stride < GN || (z && z_row_stride < d->nheads))) return SSD_ERR_SHAPE;
+    if (tokens && !selective_strides_ok(d, x_row_stride, bc_row_stride, z ? z_row_stride : 0)) return SSD_ERR_UNSUPPORTED;
     if (tokens && !stride_ok(bc_row_stride, d->act_dtype)) return SSD_ERR_ALIGN;
     for (const void* p : {B, C})
         if (p && !aligned16(p)) return SSD_ERR_ALIGN;
