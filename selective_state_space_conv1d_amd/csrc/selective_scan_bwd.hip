@@ -7,308 +7,531 @@
 //
 // Three launches.  (1) states: the forward recurrence alone, which leaves the state at the start of
 // every tile of T tokens in the workspace.  (2) gradients: tiles from last to first; each tile's a and q
-// are recomputed into registers (T x S = 64 of each) on the way forward and used on the way back.
-// (3) sums: partial sums to dA, dDskip, ddt_bias, dB and dC, in a fixed order, so results do not
-// depend on scheduling.
+// are recomputed into registers (64 of each) on the way forward and used on the way back.  (3) sums:
+// partial sums to dA, dDskip, ddt_bias, dB and dC, in a fixed order, so results do not depend on
+// scheduling.  Long sequences are cut into chunks as in the forward: then (1) runs every chunk from a
+// zero state and also leaves what a chunk's own outputs make of the gradient at its start, and (2)
+// first derives the chunk's true state and gradient at its ends from those of the other chunks.
 //
-// The layout is the forward's: lane = channel, wave = S of the N states.  Sums over states stay in the
-// lane; sums over channels (dB, dC: one value of each per token and state from 64 lanes) would cost
-// more vector operations than everything else, so the matrix pipe takes them: with the values as the
-// 16x4 operand and a one-hot 4x16 operand, v_mfma_f32_16x16x4_f32 adds lanes 16 apart into the column
-// the one-hot names, in fp32; a tile's 64 (token, state) pairs fill four 16x16 accumulators, whose rows
-// are then added by 3 additions and 2 lane exchanges.  (A product that is not finite makes the other
-// tokens of its tile and column group non-finite too: 0 times infinity.)
+// The layout is the forward's: lane = channel (CPL of them, 64 apart), wave = S of the N states.  Sums
+// over states stay in the lane; sums over channels (dB, dC: one value of each per token and state from
+// 64 lanes) would cost more vector operations than everything else, so the matrix pipe takes them: with
+// the values as the 16x4 operand and a one-hot 4x16 operand, v_mfma_f32_16x16x4_f32 adds lanes 16
+// apart into the column the one-hot names, in fp32; a tile's T S (token, state) pairs fill T S / 16
+// accumulators, whose rows are then added by 3 additions and half-wave and row exchanges.  (A product
+// that is not finite makes the other tokens of its tile non-finite too: 0 times infinity.)
 #include "selective_device.h"
 
 namespace ssd {
 
-template <typename T, int S>
-__device__ __forceinline__ void load_uniform(const T* p, float (&o)[S]) {
-    ScalarWord* q = (ScalarWord*)(uintptr_t)p;
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int i = 0; i < S / 2; ++i) {
-            const uint32_t v = q[i];
-            o[2 * i] = __uint_as_float(v << 16);
-            o[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < S; ++i) o[i] = __uint_as_float(q[i]);
-    }
-}
+// States a lane, waves, channels a lane and tokens a tile (S T CPL = 64) for N states.
+template <int N> struct SelGradShape;
+template <> struct SelGradShape<16> { static constexpr int S = 4, W = 4, CPL = 2, T = 8; };
+template <> struct SelGradShape<32> { static constexpr int S = 8, W = 4, CPL = 1, T = 8; };
+template <> struct SelGradShape<64> { static constexpr int S = 8, W = 8, CPL = 1, T = 8; };
+template <> struct SelGradShape<128> { static constexpr int S = 16, W = 8, CPL = 1, T = 4; };
 
-template <int S>
-struct SelTile {
-    static constexpr int T = 64 / S;   // tokens per tile: 64 (token, state) pairs a lane
-};
+// Below this many waves of the gradients launch sequences are cut into chunks.
+constexpr int64_t kGradWaves = 2048;
 
-// Offsets in floats of the workspace's parts.
+constexpr int kStatesTile = 16;   // tokens staged at a time by the states launch
+
+// Offsets in floats of the workspace's parts, and the chunks.
 struct SelBwdLayout {
-    int64_t ckpt, dA, dD, dbias, dBC, total;
-    int64_t tiles, blocks;
+    int64_t ckpt, tsum, ends, grads, csum, dA, dD, dbias, dBC, total;
+    int64_t tiles, blocks;   // tiles of a sequence; channel blocks of the gradients launch
+    int64_t tokens;          // of a chunk
+    int chunks;
 };
-static SelBwdLayout bwd_layout(int64_t batch, int64_t L, int64_t D, int64_t G, int64_t N) {
-    const int64_t S = N == 16 ? 4 : N == 32 ? 8 : N == 64 ? 8 : 16, T = 64 / S;
+
+template <int N>
+static SelBwdLayout layout_n(int64_t batch, int64_t L, int64_t D, int64_t G) {
+    typedef SelGradShape<N> Z;
     SelBwdLayout l;
-    l.tiles = (L + T - 1) / T;
-    l.blocks = G * ((D / G + 63) / 64);
+    l.tiles = (L + Z::T - 1) / Z::T;
+    l.blocks = G * ((D / G + 64 * Z::CPL - 1) / (64 * Z::CPL));
+    const int64_t waves = batch * l.blocks * Z::W;
+    int64_t n = waves >= kGradWaves || waves == 0 ? 1 : (kGradWaves + waves - 1) / waves;
+    if (n > L / 64) n = L / 64 > 0 ? L / 64 : 1;
+    l.tokens = n == 1 ? (L > 0 ? L : 1) : ((L + n - 1) / n + kStatesTile - 1) / kStatesTile * kStatesTile;
+    l.chunks = static_cast<int>(L > 0 ? (L + l.tokens - 1) / l.tokens : 1);
     int64_t at = 0;
     auto take = [&](int64_t n) {
         const int64_t o = at;
         at += (n + 3) & ~INT64_C(3);
         return o;
     };
+    const bool split = l.chunks > 1;
     l.ckpt = take(batch * l.tiles * N * D);
-    l.dA = take(batch * N * D);
-    l.dD = take(batch * D);
-    l.dbias = take(batch * D);
+    l.tsum = take(split ? batch * l.tiles * D : 0);
+    l.ends = take(split ? batch * l.chunks * N * D : 0);
+    l.grads = take(split ? batch * l.chunks * N * D : 0);
+    l.csum = take(split ? batch * l.chunks * D : 0);
+    l.dA = take(batch * l.chunks * N * D);
+    l.dD = take(batch * l.chunks * D);
+    l.dbias = take(batch * l.chunks * D);
     l.dBC = take(l.blocks * batch * L * 2 * N);
     l.total = at;
     return l;
 }
-
-template <typename T_, int S, int W>
-__global__ __launch_bounds__(64 * W) void selective_states_kernel(SelBwdArgs a, float* ckpt, int64_t tiles) {
-    constexpr int N = S * W, T = SelTile<S>::T, TPT = (T + W - 1) / W;
-    __shared__ float2 st[2][T][64];
-    const SelBlock k = sel_block(blockIdx.x, a.channels, a.ngroups);
-    const int lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c = k.c0 + lane;
-    const bool ok = c < k.cend;
-    const int cs = ok ? c : k.c0;
-    const int64_t L = a.seqlen, D = a.channels;
-    const T_* xp = static_cast<const T_*>(a.x) + k.b * L * a.x_row_stride + cs;
-    const T_* dp = static_cast<const T_*>(a.dt) + k.b * L * D + cs;
-    const T_* Bp = static_cast<const T_*>(a.B) + k.b * L * a.bc_row_stride + k.g * N + w * S;
-    const SelDt dtp{a.dtp.bias ? a.dtp.bias[cs] : 0.f, a.dtp.lo, a.dtp.hi, a.dtp.softplus};
-    float A2[S], h[S];
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        A2[s] = a.A[static_cast<int64_t>(cs) * N + w * S + s] * kLog2e;
-        h[s] = a.init_state && ok ? a.init_state[(k.b * D + cs) * N + w * S + s] : 0.f;
-    }
-    float xr[TPT], dr[TPT];
-    auto load = [&](int64_t t0) {
-#pragma unroll
-        for (int i = 0; i < TPT; ++i) {
-            const int64_t t = t0 + w + W * i < L ? t0 + w + W * i : L - 1;
-            xr[i] = static_cast<float>(xp[t * a.x_row_stride]);
-            dr[i] = static_cast<float>(dp[t * D]);
-        }
-    };
-    if (L > 0) load(0);
-    int buf = 0;
-    for (int64_t tile = 0; tile < tiles; ++tile, buf ^= 1) {
-        const int64_t t0 = tile * T;
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (ok) ckpt[((k.b * tiles + tile) * N + w * S + s) * D + c] = h[s];
-        if (tile + 1 == tiles) break;
-#pragma unroll
-        for (int i = 0; i < TPT; ++i) {
-            const int t = w + W * i;
-            if (t < T) {
-                const float dt = sel_dt(dr[i], dtp);
-                st[buf][t][lane] = ok ? make_float2(dt, dt * xr[i]) : make_float2(0.f, 0.f);
-            }
-        }
-        __syncthreads();
-        load(t0 + T);
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            float Bv[S];
-            load_uniform<T_, S>(Bp + (t0 + t) * a.bc_row_stride, Bv);
-            const float2 d = st[buf][t][lane];
-#pragma unroll
-            for (int s = 0; s < S; ++s) h[s] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[s]), h[s], d.y * Bv[s]);
-        }
+static SelBwdLayout bwd_layout(int64_t batch, int64_t L, int64_t D, int64_t G, int64_t N) {
+    switch (N) {
+        case 16: return layout_n<16>(batch, L, D, G);
+        case 32: return layout_n<32>(batch, L, D, G);
+        case 64: return layout_n<64>(batch, L, D, G);
+        default: return layout_n<128>(batch, L, D, G);
     }
 }
 
-template <typename T_, typename TY, int S, int W, bool GATE>
-__global__ __launch_bounds__(64 * W, 2) void selective_grad_kernel(SelBwdArgs a, float* ws, SelBwdLayout lay) {
-    constexpr int N = S * W, T = SelTile<S>::T, TPT = (T + W - 1) / W;
-    __shared__ float2 st[T][64];            // dt, dt * x
-    __shared__ float sdy[T][64];            // dy
-    __shared__ float2 part[W][T][64];       // <g, B>, <g q, A> over the wave's states
-    __shared__ float ypart[GATE ? W : 1][GATE ? T : 1][64];
-    const SelBlock k = sel_block(blockIdx.x, a.channels, a.ngroups);
+// The sum over the two half waves of x in the lower half of the result, that of y in the upper.
+__device__ __forceinline__ float add_halves(float x, float y) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// In each half wave, the sum over the two rows of 16 lanes of x in the first row, that of y in the second.
+__device__ __forceinline__ float add_rows(float x, float y) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// (1) SPLIT: chunks from a zero state, with the sums of dt and the gradients at their starts.
+template <typename T_, typename TY, int S, int W, int T, bool SPLIT, bool GATE>
+__global__ __launch_bounds__(64 * W) void selective_states_kernel(SelBwdArgs a, float* ws, SelBwdLayout lay) {
+    constexpr int N = S * W, TPT = kStatesTile / W, E = sizeof(T_);
+    constexpr int SUB = SelRows<T_, S>::n;
+    __shared__ float2 st[2][kStatesTile][64];
+    __shared__ float sdy[SPLIT ? 2 : 1][SPLIT ? kStatesTile : 1][64];
+    const int64_t per_chunk = a.batch * sel_blocks(a.channels, a.ngroups);
+    const int chunk = static_cast<int>(blockIdx.x / per_chunk);
+    const SelBlock k = sel_block(blockIdx.x % per_chunk, a.channels, a.ngroups);
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = k.c0 + lane;
     const bool ok = c < k.cend;
     const int cs = ok ? c : k.c0;
-    const int64_t L = a.seqlen, D = a.channels;
-    const T_* xp = static_cast<const T_*>(a.x) + k.b * L * a.x_row_stride + cs;
-    const T_* zp = GATE ? static_cast<const T_*>(a.z) + k.b * L * a.z_row_stride + cs : nullptr;
-    const T_* dp = static_cast<const T_*>(a.dt) + k.b * L * D + cs;
-    const TY* gp = static_cast<const TY*>(a.dy) + k.b * L * D + cs;
-    const T_* Bp = static_cast<const T_*>(a.B) + k.b * L * a.bc_row_stride + k.g * N + w * S;
-    const T_* Cp = static_cast<const T_*>(a.C) + k.b * L * a.bc_row_stride + k.g * N + w * S;
-    T_* dxp = static_cast<T_*>(a.dx) + k.b * L * D + cs;
-    T_* ddp = static_cast<T_*>(a.ddt) + k.b * L * D + cs;
-    T_* dzp = GATE ? static_cast<T_*>(a.dz) + k.b * L * D + cs : nullptr;
-    float* bcp = ws + lay.dBC + (static_cast<int64_t>(k.blk) * a.batch + k.b) * L * 2 * N + w * S;
-    const float* ckpt = ws + lay.ckpt + k.b * lay.tiles * N * D + cs;
+    const int64_t D = a.channels;
+    const int64_t r0 = k.b * a.seqlen + chunk * lay.tokens, left = a.seqlen - chunk * lay.tokens;
+    const int L = static_cast<int>(left < lay.tokens ? left : lay.tokens);
+    const char* xp = static_cast<const char*>(a.x) + (r0 * a.x_row_stride + k.c0) * E;
+    const char* dp = static_cast<const char*>(a.dt) + (r0 * D + k.c0) * E;
+    const char* zp = SPLIT && GATE ? static_cast<const char*>(a.z) + (r0 * a.z_row_stride + k.c0) * E : nullptr;
+    const char* gp = SPLIT ? static_cast<const char*>(a.dy) + (r0 * D + k.c0) * sizeof(TY) : nullptr;
+    const char* Bp = static_cast<const char*>(a.B) + (r0 * a.bc_row_stride + k.g * N + w * S) * E;
+    const char* Cp = static_cast<const char*>(a.C) + (r0 * a.bc_row_stride + k.g * N + w * S) * E;
+    const uint32_t xs = static_cast<uint32_t>(a.x_row_stride) * E, zs = static_cast<uint32_t>(a.z_row_stride) * E;
+    const uint32_t ds = static_cast<uint32_t>(D) * E, gs = static_cast<uint32_t>(D) * sizeof(TY);
+    const uint32_t bs = static_cast<uint32_t>(a.bc_row_stride) * E;
+    const uint32_t le = (cs - k.c0) * E, ge = (cs - k.c0) * sizeof(TY);
     const SelDt dtp{a.dtp.bias ? a.dtp.bias[cs] : 0.f, a.dtp.lo, a.dtp.hi, a.dtp.softplus};
-    const float Dv = a.D ? a.D[cs] : 0.f;
-    float A2[S], dA[S], carry[S];
-    const int64_t so = (k.b * D + cs) * N + w * S;
+    float A2[S], h[S], p[S], gr[S], dsum = 0.f;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         A2[s] = a.A[static_cast<int64_t>(cs) * N + w * S + s] * kLog2e;
-        dA[s] = 0.f;
-        carry[s] = a.dfinal_state && ok ? a.dfinal_state[so + s] : 0.f;
+        h[s] = !SPLIT && a.init_state ? a.init_state[(k.b * D + cs) * N + w * S + s] : 0.f;
+        p[s] = 1.f;
+        gr[s] = 0.f;
     }
-    float dDv = 0.f, dbv = 0.f;
-    for (int64_t tile = lay.tiles - 1; tile >= 0; --tile) {
-        const int64_t t0 = tile * T;
-        float xk[TPT], vk[TPT], yk[TPT], zk[TPT], dk[TPT];
+    T_ xr[TPT], dr[TPT], zr[TPT];
+    TY gv[TPT];
+    uint32_t ahead = 0;
+    auto load = [&](int first, int last) {
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
-            const int t = w + W * i;
-            const bool in = t < T && t0 + t < L && ok;
-            const int64_t tt = t0 + t < L ? t0 + t : L - 1;
-            xk[i] = in ? static_cast<float>(xp[tt * a.x_row_stride]) : 0.f;
-            vk[i] = static_cast<float>(dp[tt * D]);
-            yk[i] = in ? static_cast<float>(gp[tt * D]) : 0.f;
-            zk[i] = GATE ? static_cast<float>(zp[tt * a.z_row_stride]) : 0.f;
-            dk[i] = in ? sel_dt(vk[i], dtp) : 0.f;
-            if (t < T) {
-                st[t][lane] = make_float2(dk[i], dk[i] * xk[i]);
-                sdy[t][lane] = GATE ? yk[i] * silu_f(zk[i]) : yk[i];
-            }
+            const uint32_t t = static_cast<uint32_t>(first + w + W * i < last ? first + w + W * i : last);
+            xr[i] = *reinterpret_cast<const T_*>(xp + static_cast<uint64_t>(t * xs) + le);
+            dr[i] = *reinterpret_cast<const T_*>(dp + static_cast<uint64_t>(t * ds) + le);
+            if constexpr (SPLIT) gv[i] = *reinterpret_cast<const TY*>(gp + static_cast<uint64_t>(t * gs) + ge);
+            if constexpr (SPLIT && GATE) zr[i] = *reinterpret_cast<const T_*>(zp + static_cast<uint64_t>(t * zs) + le);
         }
-        float h[S], q[T][S], ea[T][S];
-#pragma unroll
-        for (int s = 0; s < S; ++s) h[s] = ok ? ckpt[(tile * N + w * S + s) * D] : 0.f;
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const int64_t row = t0 + t < L ? t0 + t : L - 1;
-            float Bv[S], Cv[S];
-            load_uniform<T_, S>(Bp + row * a.bc_row_stride, Bv);
-            if constexpr (GATE) load_uniform<T_, S>(Cp + row * a.bc_row_stride, Cv);
-            const float2 d = st[t][lane];
-            float y = 0.f;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                ea[t][s] = __builtin_amdgcn_exp2f(d.x * A2[s]);
-                q[t][s] = ea[t][s] * h[s];
-                h[s] = fmaf(d.y, Bv[s], q[t][s]);
-                if constexpr (GATE) y = fmaf(h[s], Cv[s], y);
-            }
-            if constexpr (GATE) ypart[w][t][lane] = y;
-        }
-        f32x4 accB[4], accC[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) accB[m] = accC[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int t = T - 1; t >= 0; --t) {
-            const int64_t row = t0 + t < L ? t0 + t : L - 1;
-            float Bv[S], Cv[S];
-            load_uniform<T_, S>(Bp + row * a.bc_row_stride, Bv);
-            load_uniform<T_, S>(Cp + row * a.bc_row_stride, Cv);
-            const float2 d = st[t][lane];
-            const float dy = sdy[t][lane];
-            float gB = 0.f, gA = 0.f;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const int f = s * T + t;   // the pair's place: accumulator f / 16, column f % 16
-                const float hot = (lane & 15) == (f & 15) ? 1.f : 0.f;
-                const float g = fmaf(Cv[s], dy, carry[s]);
-                const float hv = fmaf(d.y, Bv[s], q[t][s]);
-                accB[f >> 4] = __builtin_amdgcn_mfma_f32_16x16x4f32(g * d.y, hot, accB[f >> 4], 0, 0, 0);
-                accC[f >> 4] = __builtin_amdgcn_mfma_f32_16x16x4f32(dy * hv, hot, accC[f >> 4], 0, 0, 0);
-                gB = fmaf(g, Bv[s], gB);
-                const float v = g * q[t][s];
-                dA[s] = fmaf(d.x, v, dA[s]);
-                gA = fmaf(A2[s], v, gA);
-                carry[s] = ea[t][s] * g;
-            }
-            part[w][t][lane] = make_float2(gB, gA);
-        }
-        // rows of the accumulators: 4 in the lane, then lanes 16 and 32 apart; row r of lanes stores
-        // accumulator r
-        float vB = 0.f, vC = 0.f;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            float b = (accB[m][0] + accB[m][1]) + (accB[m][2] + accB[m][3]);
-            float e = (accC[m][0] + accC[m][1]) + (accC[m][2] + accC[m][3]);
-            b += __shfl_xor(b, 16, 64);
-            e += __shfl_xor(e, 16, 64);
-            b += __shfl_xor(b, 32, 64);
-            e += __shfl_xor(e, 32, 64);
-            if ((lane >> 4) == m) {
-                vB = b;
-                vC = e;
-            }
-        }
-        {
-            const int t = lane % T, s = lane / T;   // lane = 16 m + column
-            if (t0 + t < L) {
-                bcp[(t0 + t) * 2 * N + s] = vB;
-                bcp[(t0 + t) * 2 * N + N + s] = vC;
-            }
-        }
-        __syncthreads();
+        const uint32_t t = static_cast<uint32_t>(first + (lane & 15) < last ? first + (lane & 15) : last);
+        ahead = *reinterpret_cast<const uint32_t*>((SPLIT && (lane & 16) ? Cp : Bp) + static_cast<uint64_t>(t * bs));
+    };
+    SelRows<T_, S> rows[2];
+    float2 d[2][SUB];
+    float y[2][SUB];
+    load(0, L - 1);
+    rows[0].template load<SPLIT>(Bp, Cp, bs, 0, L - 1);
+    float* cp = ws + lay.ckpt + ((k.b * lay.tiles + chunk * (lay.tokens / T)) * N + w * S) * D + cs;
+    float* tp = ws + lay.tsum + (k.b * lay.tiles + chunk * (lay.tokens / T)) * D + cs;
+    int buf = 0;
+    for (int t0 = 0; t0 < L; t0 += kStatesTile, buf ^= 1) {
+        const int last = L - 1 - t0;
+        float xn[TPT], dn[TPT], yn[TPT];
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
-            const int t = w + W * i;
-            if (t >= T || t0 + t >= L || !ok) continue;
-            float gB = 0.f, gA = 0.f;
+            xn[i] = static_cast<float>(xr[i]);
+            dn[i] = static_cast<float>(dr[i]);
+            yn[i] = 0.f;
+            if constexpr (SPLIT) yn[i] = static_cast<float>(gv[i]);
+            if constexpr (SPLIT && GATE) yn[i] *= silu_f(static_cast<float>(zr[i]));
+        }
+        asm volatile("" ::"v"(ahead));
+        sel_dts(dn, dtp);
+        if (last < kStatesTile - 1)
 #pragma unroll
-            for (int v = 0; v < W; ++v) {
-                gB += part[v][t][lane].x;
-                gA += part[v][t][lane].y;
-            }
-            const float dy = sdy[t][lane];
-            dxp[(t0 + t) * D] = static_cast<T_>(fmaf(Dv, dy, dk[i] * gB));
-            float dd = fmaf(gA, 1.f / kLog2e, xk[i] * gB);
-            const float v = vk[i] + dtp.bias;
-            if (dtp.lo < dtp.hi) {
-                const float u = dtp.softplus ? sel_softplus(v) : v;
-                if (!(u >= dtp.lo && u <= dtp.hi)) dd = 0.f;
-            }
-            if (dtp.softplus) dd *= __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * kLog2e));
-            ddp[(t0 + t) * D] = static_cast<T_>(dd);
-            dbv += dd;
-            dDv = fmaf(dy, xk[i], dDv);
-            if constexpr (GATE) {
-                float y = Dv * xk[i];
+            for (int i = 0; i < TPT; ++i)
+                if (w + W * i > last) xn[i] = dn[i] = yn[i] = 0.f;
 #pragma unroll
-                for (int u = 0; u < W; ++u) y += ypart[u][t][lane];
-                const float sg = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-zk[i] * kLog2e));
-                dzp[(t0 + t) * D] = static_cast<T_>(yk[i] * y * sg * fmaf(zk[i], 1.f - sg, 1.f));
-            }
+        for (int i = 0; i < TPT; ++i) {
+            st[buf][w + W * i][lane] = make_float2(dn[i], dn[i] * xn[i]);
+            if constexpr (SPLIT) sdy[buf][w + W * i][lane] = yn[i];
         }
         __syncthreads();
+        load(kStatesTile, last);
+#pragma unroll
+        for (int t = 0; t < SUB; ++t) {
+            d[0][t] = st[buf][t][lane];
+            if constexpr (SPLIT) y[0][t] = sdy[buf][t][lane];
+        }
+#pragma unroll
+        for (int u = 0; u < kStatesTile; u += SUB) {
+            const int at = (u / SUB) & 1;
+            rows[at ^ 1].template load<SPLIT>(Bp, Cp, bs, u + SUB, last);
+            if (u + SUB < kStatesTile)
+#pragma unroll
+                for (int t = 0; t < SUB; ++t) {
+                    d[at ^ 1][t] = st[buf][u + SUB + t][lane];
+                    if constexpr (SPLIT) y[at ^ 1][t] = sdy[buf][u + SUB + t][lane];
+                }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = 0; t < SUB; ++t) {
+                if ((u + t) % T == 0 && u + t <= last) {
+                    // the state at the start of a tile, and the chunk's sum of dt before it
+                    if (ok) {
+#pragma unroll
+                        for (int s = 0; s < S; ++s) cp[static_cast<int64_t>((u + t) / T * N + s) * D] = h[s];
+                        if (SPLIT && w == 0) tp[static_cast<int64_t>((u + t) / T) * D] = dsum;
+                    }
+                }
+                if constexpr (SPLIT) dsum += d[at][t].x;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const float e = __builtin_amdgcn_exp2f(d[at][t].x * A2[s]);
+                    h[s] = fmaf(e, h[s], d[at][t].y * rows[at].b(t, s));
+                    if constexpr (SPLIT) {
+                        p[s] *= e;
+                        gr[s] = fmaf(p[s], rows[at].c(t, s) * y[at][t], gr[s]);
+                    }
+                }
+            }
+        }
+        xp += static_cast<int64_t>(kStatesTile) * xs;
+        dp += static_cast<int64_t>(kStatesTile) * ds;
+        if constexpr (SPLIT) gp += static_cast<int64_t>(kStatesTile) * gs;
+        if constexpr (SPLIT && GATE) zp += static_cast<int64_t>(kStatesTile) * zs;
+        Bp += static_cast<int64_t>(kStatesTile) * bs;
+        Cp += static_cast<int64_t>(kStatesTile) * bs;
+        cp += static_cast<int64_t>(kStatesTile / T) * N * D;
+        tp += static_cast<int64_t>(kStatesTile / T) * D;
     }
-    if (ok) {
+    if (SPLIT && ok) {
+        const int64_t bc = k.b * lay.chunks + chunk;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            ws[lay.dA + (k.b * N + w * S + s) * D + c] = dA[s];
-            if (a.dinit_state) a.dinit_state[so + s] = carry[s];
+            ws[lay.ends + (bc * N + w * S + s) * D + c] = h[s];
+            ws[lay.grads + (bc * N + w * S + s) * D + c] = gr[s];
         }
-    }
-    part[w][0][lane] = make_float2(dDv, dbv);   // the last tile ended with a barrier
-    __syncthreads();
-    if (w == 0 && ok) {
-        float u = 0.f, v = 0.f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            u += part[i][0][lane].x;
-            v += part[i][0][lane].y;
-        }
-        ws[lay.dD + k.b * D + c] = u;
-        ws[lay.dbias + k.b * D + c] = v;
+        if (w == 0) ws[lay.csum + bc * D + c] = dsum;
     }
 }
 
-// Sums of the partial results: D N values of dA, D of dDskip and of ddt_bias over the batch, and
-// B L G N values of dB and of dC over the group's channel blocks.
+// What a thread keeps of its own (token, channel) from before the scan of the tile until after it.
+template <typename T, typename TY>
+struct SelRaw {
+    T x, dt, z;
+    TY dout;
+};
+
+// (2)
+template <typename T_, typename TY, int N, bool SPLIT, bool GATE>
+__global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_kernel(SelBwdArgs a, float* ws, SelBwdLayout lay) {
+    typedef SelGradShape<N> Z;
+    constexpr int S = Z::S, W = Z::W, T = Z::T, P = Z::CPL, E = sizeof(T_);
+    constexpr int TPT = (T + W - 1) / W, M = S * T / 16;
+    constexpr int SUB = SelRows<T_, S>::n < T ? SelRows<T_, S>::n : T;
+    constexpr int K = T / SUB;              // sub-tiles whose B and C are in scalar registers
+    __shared__ float2 st[T][P][64];         // dt, dt * x
+    __shared__ float sdy[T][P][64];         // dy
+    __shared__ float2 part[W][T][P][64];    // <g, B>, <g q, A2> over the wave's states
+    __shared__ SelRaw<T_, TY> raw[T][P][64];
+    __shared__ float ypart[GATE ? W : 1][GATE ? T : 1][P][64];
+    const int64_t per_chunk = a.batch * lay.blocks;
+    const int chunk = static_cast<int>(blockIdx.x / per_chunk);
+    const int64_t bb = blockIdx.x % per_chunk, b = bb / lay.blocks;
+    const int blk = static_cast<int>(bb - b * lay.blocks);
+    const int cpg = a.channels / a.ngroups, bpg = (cpg + 64 * P - 1) / (64 * P);
+    const int grp = blk / bpg, c0 = grp * cpg + (blk - grp * bpg) * 64 * P, cend = (grp + 1) * cpg;
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t D = a.channels;
+    const int64_t r0 = b * a.seqlen + chunk * lay.tokens, left = a.seqlen - chunk * lay.tokens;
+    const int L = static_cast<int>(left < lay.tokens ? left : lay.tokens);
+    const int tiles = (L + T - 1) / T;
+    int c[P];
+    bool ok[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        ok[j] = c0 + 64 * j + lane < cend;
+        c[j] = ok[j] ? c0 + 64 * j + lane : c0;   // lanes past the group: that channel's data, zero inputs, no stores
+    }
+    const uint32_t bs = static_cast<uint32_t>(a.bc_row_stride) * E;
+    const int64_t tile0 = b * lay.tiles + chunk * (lay.tokens / T);
+    SelDt dtp[P];
+    float Dv[P], A2[P][S], dA[P][S], carry[P][S], hin[SPLIT ? P : 1][S], dDv[P], dbv[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        dtp[j] = SelDt{a.dtp.bias ? a.dtp.bias[c[j]] : 0.f, a.dtp.lo, a.dtp.hi, a.dtp.softplus};
+        Dv[j] = a.D ? a.D[c[j]] : 0.f;
+        dDv[j] = dbv[j] = 0.f;
+        const int64_t so = (b * D + c[j]) * N + w * S;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            A2[j][s] = a.A[static_cast<int64_t>(c[j]) * N + w * S + s] * kLog2e;
+            dA[j][s] = 0.f;
+            carry[j][s] = a.dfinal_state && ok[j] ? a.dfinal_state[so + s] : 0.f;
+            if constexpr (SPLIT) hin[j][s] = a.init_state ? a.init_state[so + s] : 0.f;
+        }
+        if constexpr (SPLIT) {
+            for (int p = 0; p < chunk; ++p) {
+                const float sum = ws[lay.csum + (b * lay.chunks + p) * D + c[j]];
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    hin[j][s] = fmaf(__builtin_amdgcn_exp2f(sum * A2[j][s]), hin[j][s],
+                                     ws[lay.ends + ((b * lay.chunks + p) * N + w * S + s) * D + c[j]]);
+            }
+            for (int p = lay.chunks - 1; p > chunk; --p) {
+                const float sum = ws[lay.csum + (b * lay.chunks + p) * D + c[j]];
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    carry[j][s] = fmaf(__builtin_amdgcn_exp2f(sum * A2[j][s]), carry[j][s],
+                                       ws[lay.grads + ((b * lay.chunks + p) * N + w * S + s) * D + c[j]]);
+                    if (!ok[j]) carry[j][s] = 0.f;
+                }
+            }
+        }
+    }
+    T_ xr[TPT][P], dr[TPT][P], zr[TPT][P];   // the next tile's values as loaded
+    TY gv[TPT][P];
+    auto load = [&](int tile) {   // this thread's tokens w + W i of a tile, none past the chunk's last
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+            const int64_t row = r0 + (tile * T + w + W * i < L ? tile * T + w + W * i : L - 1);
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                xr[i][j] = (static_cast<const T_*>(a.x) + row * a.x_row_stride)[c[j]];
+                dr[i][j] = (static_cast<const T_*>(a.dt) + row * D)[c[j]];
+                gv[i][j] = (static_cast<const TY*>(a.dy) + row * D)[c[j]];
+                if constexpr (GATE) zr[i][j] = (static_cast<const T_*>(a.z) + row * a.z_row_stride)[c[j]];
+            }
+        }
+    };
+    float h[P][S], ts[P];
+    auto load_state = [&](int tile) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            if constexpr (SPLIT) ts[j] = ws[lay.tsum + (tile0 + tile) * D + c[j]];
+#pragma unroll
+            for (int s = 0; s < S; ++s) h[j][s] = ws[lay.ckpt + ((tile0 + tile) * N + w * S + s) * D + c[j]];
+        }
+    };
+    auto row_of = [&](const void* p, int tile) {   // this wave's states of the tile's first row of B or C
+        return static_cast<const char*>(p) + ((r0 + tile * T) * a.bc_row_stride + grp * N + w * S) * E;
+    };
+    SelRows<T_, S> rows[2];
+    if (tiles > 0) {
+        load(tiles - 1);
+        load_state(tiles - 1);
+        rows[0].template load<true>(row_of(a.B, tiles - 1), row_of(a.C, tiles - 1), bs, 0, L - 1 - (tiles - 1) * T);
+    }
+    for (int tile = tiles - 1; tile >= 0; --tile) {
+        const int last = L - 1 - tile * T;   // the tile's last row, if below T - 1
+        const char *Bp = row_of(a.B, tile), *Cp = row_of(a.C, tile);
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+            const int t = w + W * i;
+            if (T % W != 0 && t >= T) continue;
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const bool in = ok[j] && t <= last;
+                if (!in) {
+                    xr[i][j] = static_cast<T_>(0.f);
+                    gv[i][j] = static_cast<TY>(0.f);
+                }
+                float dt = sel_dt(static_cast<float>(dr[i][j]), dtp[j]);
+                if (!in) dt = 0.f;
+                float dy = static_cast<float>(gv[i][j]);
+                if constexpr (GATE) dy *= silu_f(static_cast<float>(zr[i][j]));
+                st[t][j][lane] = make_float2(dt, dt * static_cast<float>(xr[i][j]));
+                sdy[t][j][lane] = dy;
+                raw[t][j][lane] = SelRaw<T_, TY>{xr[i][j], dr[i][j], GATE ? zr[i][j] : static_cast<T_>(0.f), gv[i][j]};
+            }
+        }
+        if constexpr (SPLIT)
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+#pragma unroll
+                for (int s = 0; s < S; ++s) h[j][s] = fmaf(__builtin_amdgcn_exp2f(ts[j] * A2[j][s]), hin[j][s], h[j][s]);
+        __syncthreads();
+        float q[T][P][S], ea[T][P][S];
+#pragma unroll
+        for (int u = 0; u < K; ++u) {
+            const int at = u & 1;
+            // the way back starts with the last rows of the way forward
+            if (u + 1 < K) rows[at ^ 1].template load<true>(Bp, Cp, bs, (u + 1) * SUB, last);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int v = 0; v < SUB; ++v) {
+                const int t = u * SUB + v;
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const float2 d = st[t][j][lane];
+                    float y = 0.f;
+#pragma unroll
+                    for (int s = 0; s < S; ++s) {
+                        ea[t][j][s] = __builtin_amdgcn_exp2f(d.x * A2[j][s]);
+                        q[t][j][s] = ea[t][j][s] * h[j][s];
+                        h[j][s] = fmaf(d.y, rows[at].b(v, s), q[t][j][s]);
+                        if constexpr (GATE) y = fmaf(h[j][s], rows[at].c(v, s), y);
+                    }
+                    if constexpr (GATE) ypart[w][t][j][lane] = y;
+                }
+            }
+        }
+        // the next tile's loads; h is free from here on
+        load(tile > 0 ? tile - 1 : 0);
+        load_state(tile > 0 ? tile - 1 : 0);
+        f32x4 accB[M], accC[M];
+#pragma unroll
+        for (int m = 0; m < M; ++m) accB[m] = accC[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = K - 1; u >= 0; --u) {
+            const int at = u & 1;
+            if (u > 0) rows[at ^ 1].template load<true>(Bp, Cp, bs, (u - 1) * SUB, last);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int v = SUB - 1; v >= 0; --v) {
+                const int t = u * SUB + v;
+                float pB[S], pC[S];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const float2 d = st[t][j][lane];
+                    const float dy = sdy[t][j][lane];
+                    float gB = 0.f, gA = 0.f;
+#pragma unroll
+                    for (int s = 0; s < S; ++s) {
+                        const float g = fmaf(rows[at].c(v, s), dy, carry[j][s]);
+                        const float hv = fmaf(d.y, rows[at].b(v, s), q[t][j][s]);
+                        pB[s] = j == 0 ? g * d.y : fmaf(g, d.y, pB[s]);
+                        pC[s] = j == 0 ? dy * hv : fmaf(dy, hv, pC[s]);
+                        gB = fmaf(g, rows[at].b(v, s), gB);
+                        const float x = g * q[t][j][s];
+                        dA[j][s] = fmaf(d.x, x, dA[j][s]);
+                        gA = fmaf(A2[j][s], x, gA);
+                        carry[j][s] = ea[t][j][s] * g;
+                    }
+                    part[w][t][j][lane] = make_float2(gB, gA);
+                }
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const int f = s * T + t;   // the pair's place: accumulator f / 16, column f % 16
+                    const float hot = (lane & 15) == (f & 15) ? 1.f : 0.f;
+                    accB[f >> 4] = __builtin_amdgcn_mfma_f32_16x16x4f32(pB[s], hot, accB[f >> 4], 0, 0, 0);
+                    accC[f >> 4] = __builtin_amdgcn_mfma_f32_16x16x4f32(pC[s], hot, accC[f >> 4], 0, 0, 0);
+                }
+            }
+        }
+        // Rows of the accumulators: 4 in the lane; the other sums by exchanging half waves and rows
+        // between two sums at a time, which leaves four pairs' sums in the four rows of one register.
+        float* bcp = ws + lay.dBC + (static_cast<int64_t>(blk) * a.batch * a.seqlen + r0 + tile * T) * 2 * N + w * S;
+        float sums[2 * M];
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            sums[m] = (accB[m][0] + accB[m][1]) + (accB[m][2] + accB[m][3]);
+            sums[M + m] = (accC[m][0] + accC[m][1]) + (accC[m][2] + accC[m][3]);
+        }
+#pragma unroll
+        for (int m = 0; m < 2 * M; m += 4) {
+            const float v = add_rows(add_halves(sums[m], sums[m + 1]), add_halves(sums[m + 2], sums[m + 3]));
+            // row 0: sum m, row 1: m + 2, row 2: m + 1, row 3: m + 3
+            const int row = lane >> 4, mm = m + (row == 1 ? 2 : row == 2 ? 1 : row);
+            const int f = (mm % M) * 16 + (lane & 15), t = f % T, s = f / T;
+            if (t <= last) bcp[static_cast<uint32_t>(t * 2 * N + mm / M * N + s)] = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+            const int t = w + W * i;
+            if (t >= T || t > last) continue;
+            const int64_t out = (r0 + tile * T + t) * D;
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const SelRaw<T_, TY> r = raw[t][j][lane];
+                const float x = static_cast<float>(r.x), v = static_cast<float>(r.dt) + dtp[j].bias;
+                float gB = 0.f, gA = 0.f, y = Dv[j] * x;
+#pragma unroll
+                for (int u = 0; u < W; ++u) {
+                    const float2 pp = part[u][t][j][lane];
+                    gB += pp.x;
+                    gA += pp.y;
+                    if constexpr (GATE) y += ypart[u][t][j][lane];
+                }
+                const float dy = sdy[t][j][lane], dt = st[t][j][lane].x;
+                const float dx = fmaf(Dv[j], dy, dt * gB);
+                float dd = fmaf(gA, 1.f / kLog2e, x * gB);
+                if (dtp[j].lo < dtp[j].hi) {
+                    const float u = dtp[j].softplus ? sel_softplus(v) : v;
+                    if (!(u >= dtp[j].lo && u <= dtp[j].hi)) dd = 0.f;
+                }
+                if (dtp[j].softplus) dd *= __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * kLog2e));
+                if (!ok[j]) dd = 0.f;
+                dbv[j] += dd;
+                dDv[j] = fmaf(dy, x, dDv[j]);
+                float dz = 0.f;
+                if constexpr (GATE) {
+                    const float z = static_cast<float>(r.z);
+                    const float sg = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * kLog2e));
+                    dz = static_cast<float>(r.dout) * y * sg * fmaf(z, 1.f - sg, 1.f);
+                }
+                if (ok[j]) {
+                    (static_cast<T_*>(a.dx) + out)[c[j]] = static_cast<T_>(dx);
+                    (static_cast<T_*>(a.ddt) + out)[c[j]] = static_cast<T_>(dd);
+                    if constexpr (GATE) (static_cast<T_*>(a.dz) + out)[c[j]] = static_cast<T_>(dz);
+                }
+            }
+        }
+        if (tile > 0) rows[0].template load<true>(row_of(a.B, tile - 1), row_of(a.C, tile - 1), bs, 0, T - 1);
+        __syncthreads();
+    }
+    const int64_t bc = b * lay.chunks + chunk;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        part[w][0][j][lane] = make_float2(dDv[j], dbv[j]);   // the last tile ended with a barrier
+        if (!ok[j]) continue;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            ws[lay.dA + (bc * N + w * S + s) * D + c[j]] = dA[j][s];
+            if (a.dinit_state && chunk == 0) a.dinit_state[(b * D + c[j]) * N + w * S + s] = carry[j][s];
+        }
+    }
+    __syncthreads();
+    if (w == 0)
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            if (!ok[j]) continue;
+            float u = 0.f, v = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                u += part[i][0][j][lane].x;
+                v += part[i][0][j][lane].y;
+            }
+            ws[lay.dD + bc * D + c[j]] = u;
+            ws[lay.dbias + bc * D + c[j]] = v;
+        }
+}
+
+// (3) D N values of dA, D of dDskip and of ddt_bias over batch and chunks, and B L G N values of dB and
+// of dC over the group's channel blocks.
 template <typename T>
 __global__ __launch_bounds__(256) void selective_sums_kernel(SelBwdArgs a, const float* __restrict__ ws, SelBwdLayout lay) {
     const int64_t D = a.channels, N = a.d_state, G = a.ngroups, rows = a.batch * a.seqlen;
@@ -317,7 +540,7 @@ __global__ __launch_bounds__(256) void selective_sums_kernel(SelBwdArgs a, const
         const float* p = ws + (i < N * D ? lay.dA + i : i < (N + 1) * D ? lay.dD + i - N * D : lay.dbias + i - (N + 1) * D);
         const int64_t step = i < N * D ? N * D : D;
         float v = 0.f;
-        for (int64_t b = 0; b < a.batch; ++b) v += p[b * step];
+        for (int64_t b = 0; b < a.batch * lay.chunks; ++b) v += p[b * step];
         if (i < N * D) a.dA[i % D * N + i / D] = v;
         else if (i < (N + 1) * D) { if (a.dD) a.dD[i - N * D] = v; }
         else if (a.ddt_bias) a.ddt_bias[i - (N + 1) * D] = v;
@@ -333,14 +556,24 @@ __global__ __launch_bounds__(256) void selective_sums_kernel(SelBwdArgs a, const
     (which ? static_cast<T*>(a.dC) : static_cast<T*>(a.dB))[(row * G + g) * N + n] = static_cast<T>(v);
 }
 
-template <typename T, typename TY, int S, int W>
-static hipError_t bwd_launch(const SelBwdArgs& a, float* ws, const SelBwdLayout& lay, hipStream_t s) {
-    const dim3 grid(static_cast<uint32_t>(a.batch * lay.blocks)), block(64 * W);
+template <typename T, typename TY, int N, bool SPLIT, bool GATE>
+static void bwd_main(const SelBwdArgs& a, float* ws, const SelBwdLayout& lay, hipStream_t s) {
+    typedef SelGradShape<N> Z;
+    constexpr int W = N == 128 ? 8 : 4, S = N / W;   // the states launch's waves and states a lane
+    const dim3 g1(static_cast<uint32_t>(a.batch * sel_blocks(a.channels, a.ngroups) * lay.chunks));
+    const dim3 g2(static_cast<uint32_t>(a.batch * lay.blocks * lay.chunks));
+    if (a.seqlen > 0)
+        hipLaunchKernelGGL((selective_states_kernel<T, TY, S, W, Z::T, SPLIT, GATE>), g1, dim3(64 * W), 0, s, a, ws, lay);
+    hipLaunchKernelGGL((selective_grad_kernel<T, TY, N, SPLIT, GATE>), g2, dim3(64 * Z::W), 0, s, a, ws, lay);
+}
+
+template <typename T, typename TY, int N>
+static hipError_t bwd_n(const SelBwdArgs& a, float* ws, hipStream_t s) {
+    const SelBwdLayout lay = bwd_layout(a.batch, a.seqlen, a.channels, a.ngroups, a.d_state);
     if (a.batch > 0) {
-        hipLaunchKernelGGL((selective_states_kernel<T, S, W>), grid, block, 0, s, a, ws + lay.ckpt, lay.tiles);
+        if (lay.chunks > 1) a.z ? bwd_main<T, TY, N, true, true>(a, ws, lay, s) : bwd_main<T, TY, N, true, false>(a, ws, lay, s);
+        else a.z ? bwd_main<T, TY, N, false, true>(a, ws, lay, s) : bwd_main<T, TY, N, false, false>(a, ws, lay, s);
     }
-    if (a.batch > 0 && a.z) hipLaunchKernelGGL((selective_grad_kernel<T, TY, S, W, true>), grid, block, 0, s, a, ws, lay);
-    else if (a.batch > 0) hipLaunchKernelGGL((selective_grad_kernel<T, TY, S, W, false>), grid, block, 0, s, a, ws, lay);
     const int64_t n = (a.d_state + 2) * static_cast<int64_t>(a.channels) + a.batch * a.seqlen * 2 * a.ngroups * a.d_state;
     hipLaunchKernelGGL((selective_sums_kernel<T>), dim3(static_cast<uint32_t>((n + 255) / 256)), dim3(256), 0, s, a, ws, lay);
     return hipGetLastError();
@@ -348,12 +581,11 @@ static hipError_t bwd_launch(const SelBwdArgs& a, float* ws, const SelBwdLayout&
 
 template <typename T, typename TY>
 static hipError_t bwd_t(const SelBwdArgs& a, float* ws, hipStream_t s) {
-    const SelBwdLayout lay = bwd_layout(a.batch, a.seqlen, a.channels, a.ngroups, a.d_state);
     switch (a.d_state) {
-        case 16: return bwd_launch<T, TY, 4, 4>(a, ws, lay, s);
-        case 32: return bwd_launch<T, TY, 8, 4>(a, ws, lay, s);
-        case 64: return bwd_launch<T, TY, 8, 8>(a, ws, lay, s);
-        case 128: return bwd_launch<T, TY, 16, 8>(a, ws, lay, s);
+        case 16: return bwd_n<T, TY, 16>(a, ws, s);
+        case 32: return bwd_n<T, TY, 32>(a, ws, s);
+        case 64: return bwd_n<T, TY, 64>(a, ws, s);
+        case 128: return bwd_n<T, TY, 128>(a, ws, s);
         default: return hipErrorInvalidValue;
     }
 }
