@@ -402,6 +402,8 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
         load(tile > 0 ? tile - 1 : 0);
         load_state(tile > 0 ? tile - 1 : 0);
         f32x4 accB[M], accC[M];
+        int col = lane & 15;
+        asm volatile("" : "+v"(col));   // the one-hot operands are made where they are used: kept, they spill
 #pragma unroll
         for (int m = 0; m < M; ++m) accB[m] = accC[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -435,12 +437,17 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
 #pragma unroll
                 for (int s = 0; s < S; ++s) {
                     const int f = s * T + t;   // the pair's place: accumulator f / 16, column f % 16
-                    const float hot = (lane & 15) == (f & 15) ? 1.f : 0.f;
+                    const float hot = col == (f & 15) ? 1.f : 0.f;
                     accB[f >> 4] = __builtin_amdgcn_mfma_f32_16x16x4f32(pB[s], hot, accB[f >> 4], 0, 0, 0);
                     accC[f >> 4] = __builtin_amdgcn_mfma_f32_16x16x4f32(pC[s], hot, accC[f >> 4], 0, 0, 0);
                 }
             }
         }
+        // dA's products are added here and not, as the compiler would have it, after the next barrier
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+#pragma unroll
+            for (int s = 0; s < S; ++s) asm volatile("" : "+v"(dA[j][s]));
         // Rows of the accumulators: 4 in the lane; the other sums by exchanging half waves and rows
         // between two sums at a time, which leaves four pairs' sums in the four rows of one register.
         float* bcp = ws + lay.dBC + (static_cast<int64_t>(blk) * a.batch * a.seqlen + r0 + tile * T) * 2 * N + w * S;
