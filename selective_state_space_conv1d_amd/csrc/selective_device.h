@@ -20,6 +20,9 @@ __device__ __forceinline__ float sel_softplus(float v) {
     const float l = u == 1.f ? e : e * (__builtin_amdgcn_logf(u) * 0.69314718055994530942f) * __builtin_amdgcn_rcpf(u - 1.f);
     return v > 20.f ? v : l;
 }
+__device__ __forceinline__ float sel_sigmoid(float v) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * kLog2e));
+}
 template <int K>
 __device__ __forceinline__ void sel_dts(float (&v)[K], const SelDt& p) {
 #pragma unroll

@@ -236,12 +236,19 @@ __global__ __launch_bounds__(64 * W) void selective_states_kernel(SelBwdArgs a, 
     }
 }
 
-// What a thread keeps of its own (token, channel) from before the scan of the tile until after it.
-template <typename T, typename TY>
-struct SelRaw {
-    T x, dt, z;
-    TY dout;
-};
+// What a thread keeps of its own (token, channel) from before the scan of the tile until after it: x, the
+// derivative of the dt prologue, and dout silu'(z).
+template <bool GATE> struct SelKeep { float x, ddt, dz; };
+template <> struct SelKeep<false> { float x, ddt; };
+
+// The kernel's arguments read from memory again wherever this is called: kept in scalar registers over
+// the gradients kernel's loop, they would be moved to and from vector registers lane by lane.
+typedef const SelBwdArgs __attribute__((address_space(4)))* SelBwdArgsPtr;
+__device__ __forceinline__ SelBwdArgsPtr reread_args() {
+    SelBwdArgsPtr p = (SelBwdArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return p;
+}
 
 // (2)
 template <typename T_, typename TY, int N, bool SPLIT, bool GATE>
@@ -254,7 +261,7 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
     __shared__ float2 st[T][P][64];         // dt, dt * x
     __shared__ float sdy[T][P][64];         // dy
     __shared__ float2 part[W][T][P][64];    // <g, B>, <g q, A2> over the wave's states
-    __shared__ SelRaw<T_, TY> raw[T][P][64];
+    __shared__ SelKeep<GATE> keep[T][P][64];
     __shared__ float ypart[GATE ? W : 1][GATE ? T : 1][P][64];
     const int64_t per_chunk = a.batch * lay.blocks;
     const int chunk = static_cast<int>(blockIdx.x / per_chunk);
@@ -277,11 +284,11 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
     }
     const uint32_t bs = static_cast<uint32_t>(a.bc_row_stride) * E;
     const int64_t tile0 = b * lay.tiles + chunk * (lay.tokens / T);
-    SelDt dtp[P];
-    float Dv[P], A2[P][S], dA[P][S], carry[P][S], hin[SPLIT ? P : 1][S], dDv[P], dbv[P];
+    const bool ragged = c0 + 64 * P > cend;   // some lanes have no channel
+    float bias[P], Dv[P], A2[P][S], dA[P][S], carry[P][S], hin[SPLIT ? P : 1][S], dDv[P], dbv[P];
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-        dtp[j] = SelDt{a.dtp.bias ? a.dtp.bias[c[j]] : 0.f, a.dtp.lo, a.dtp.hi, a.dtp.softplus};
+        bias[j] = a.dtp.bias ? a.dtp.bias[c[j]] : 0.f;
         Dv[j] = a.D ? a.D[c[j]] : 0.f;
         dDv[j] = dbv[j] = 0.f;
         const int64_t so = (b * D + c[j]) * N + w * S;
@@ -314,15 +321,25 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
     T_ xr[TPT][P], dr[TPT][P], zr[TPT][P];   // the next tile's values as loaded
     TY gv[TPT][P];
     auto load = [&](int tile) {   // this thread's tokens w + W i of a tile, none past the chunk's last
+        const SelBwdArgsPtr ka = reread_args();
+        const int64_t row = r0 + tile * T;
+        const int last = L - 1 - tile * T;
+        const char* xp = static_cast<const char*>(ka->x) + row * ka->x_row_stride * E;
+        const char* dp = static_cast<const char*>(ka->dt) + row * D * E;
+        const char* gp = static_cast<const char*>(ka->dy) + row * D * sizeof(TY);
+        const char* zp = GATE ? static_cast<const char*>(ka->z) + row * ka->z_row_stride * E : nullptr;
+        const uint32_t xs = static_cast<uint32_t>(ka->x_row_stride) * E, zs = static_cast<uint32_t>(ka->z_row_stride) * E;
+        const uint32_t ds = static_cast<uint32_t>(D) * E, gs = static_cast<uint32_t>(D) * sizeof(TY);
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
-            const int64_t row = r0 + (tile * T + w + W * i < L ? tile * T + w + W * i : L - 1);
+            const uint32_t t = w + W * i < last ? w + W * i : last;
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                xr[i][j] = (static_cast<const T_*>(a.x) + row * a.x_row_stride)[c[j]];
-                dr[i][j] = (static_cast<const T_*>(a.dt) + row * D)[c[j]];
-                gv[i][j] = (static_cast<const TY*>(a.dy) + row * D)[c[j]];
-                if constexpr (GATE) zr[i][j] = (static_cast<const T_*>(a.z) + row * a.z_row_stride)[c[j]];
+                const uint32_t o = static_cast<uint32_t>(c[j]) * E;
+                xr[i][j] = *reinterpret_cast<const T_*>(xp + static_cast<uint64_t>(t * xs) + o);
+                dr[i][j] = *reinterpret_cast<const T_*>(dp + static_cast<uint64_t>(t * ds) + o);
+                gv[i][j] = *reinterpret_cast<const TY*>(gp + static_cast<uint64_t>(t * gs) + static_cast<uint32_t>(c[j]) * static_cast<uint32_t>(sizeof(TY)));
+                if constexpr (GATE) zr[i][j] = *reinterpret_cast<const T_*>(zp + static_cast<uint64_t>(t * zs) + o);
             }
         }
     };
@@ -346,25 +363,57 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
     }
     for (int tile = tiles - 1; tile >= 0; --tile) {
         const int last = L - 1 - tile * T;   // the tile's last row, if below T - 1
-        const char *Bp = row_of(a.B, tile), *Cp = row_of(a.C, tile);
+        const SelBwdArgsPtr kb = reread_args();
+        const char *Bp = row_of(kb->B, tile), *Cp = row_of(kb->C, tile);
+        float dt[TPT][P], slope[TPT][P], x[TPT][P], dy[TPT][P], dz[TPT][P];
+#pragma unroll
+        for (int i = 0; i < TPT; ++i)
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                x[i][j] = static_cast<float>(xr[i][j]);
+                dt[i][j] = static_cast<float>(dr[i][j]) + bias[j];
+                dy[i][j] = static_cast<float>(gv[i][j]);
+                slope[i][j] = 1.f;
+                dz[i][j] = 0.f;
+                if constexpr (GATE) {
+                    const float z = static_cast<float>(zr[i][j]), sg = sel_sigmoid(z);
+                    dz[i][j] = dy[i][j] * sg * fmaf(z, 1.f - sg, 1.f);
+                    dy[i][j] *= z * sg;
+                }
+            }
+        if (a.dtp.softplus)
+#pragma unroll
+            for (int i = 0; i < TPT; ++i)
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    slope[i][j] = sel_sigmoid(dt[i][j]);
+                    dt[i][j] = sel_softplus(dt[i][j]);
+                }
+        if (a.dtp.lo < a.dtp.hi)
+#pragma unroll
+            for (int i = 0; i < TPT; ++i)
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    if (!(dt[i][j] >= a.dtp.lo && dt[i][j] <= a.dtp.hi)) slope[i][j] = 0.f;
+                    dt[i][j] = fminf(fmaxf(dt[i][j], a.dtp.lo), a.dtp.hi);
+                }
+        if (ragged || last < T - 1)   // no token or no channel there: nothing enters any sum
+#pragma unroll
+            for (int i = 0; i < TPT; ++i)
+#pragma unroll
+                for (int j = 0; j < P; ++j)
+                    if (w + W * i > last || !ok[j]) x[i][j] = dt[i][j] = dy[i][j] = dz[i][j] = slope[i][j] = 0.f;
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
             const int t = w + W * i;
             if (T % W != 0 && t >= T) continue;
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const bool in = ok[j] && t <= last;
-                if (!in) {
-                    xr[i][j] = static_cast<T_>(0.f);
-                    gv[i][j] = static_cast<TY>(0.f);
-                }
-                float dt = sel_dt(static_cast<float>(dr[i][j]), dtp[j]);
-                if (!in) dt = 0.f;
-                float dy = static_cast<float>(gv[i][j]);
-                if constexpr (GATE) dy *= silu_f(static_cast<float>(zr[i][j]));
-                st[t][j][lane] = make_float2(dt, dt * static_cast<float>(xr[i][j]));
-                sdy[t][j][lane] = dy;
-                raw[t][j][lane] = SelRaw<T_, TY>{xr[i][j], dr[i][j], GATE ? zr[i][j] : static_cast<T_>(0.f), gv[i][j]};
+                keep[t][j][lane].x = x[i][j];
+                keep[t][j][lane].ddt = slope[i][j];
+                if constexpr (GATE) keep[t][j][lane].dz = dz[i][j];
+                st[t][j][lane] = make_float2(dt[i][j], dt[i][j] * x[i][j]);
+                sdy[t][j][lane] = dy[i][j];
             }
         }
         if constexpr (SPLIT)
@@ -466,48 +515,60 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
             if (t <= last) bcp[static_cast<uint32_t>(t * 2 * N + mm / M * N + s)] = v;
         }
         __syncthreads();
+        const SelBwdArgsPtr ka = reread_args();
+        if (T % W == 0 || w < T) {
+            float gB[TPT][P], gA[TPT][P], y[TPT][P], dx[TPT][P], dd[TPT][P];
 #pragma unroll
-        for (int i = 0; i < TPT; ++i) {
-            const int t = w + W * i;
-            if (t >= T || t > last) continue;
-            const int64_t out = (r0 + tile * T + t) * D;
+            for (int i = 0; i < TPT; ++i)
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const int t = w + W * i;
+                    gB[i][j] = gA[i][j] = y[i][j] = 0.f;
+#pragma unroll
+                    for (int u = 0; u < W; ++u) {
+                        const float2 pp = part[u][t][j][lane];
+                        gB[i][j] += pp.x;
+                        gA[i][j] += pp.y;
+                        if constexpr (GATE) y[i][j] += ypart[u][t][j][lane];
+                    }
+                }
+#pragma unroll
+            for (int i = 0; i < TPT; ++i)
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const int t = w + W * i;
+                    const SelKeep<GATE> r = keep[t][j][lane];
+                    const float dy = sdy[t][j][lane];
+                    dx[i][j] = fmaf(Dv[j], dy, st[t][j][lane].x * gB[i][j]);
+                    dd[i][j] = fmaf(gA[i][j], 1.f / kLog2e, r.x * gB[i][j]) * r.ddt;
+                    dbv[j] += dd[i][j];
+                    dDv[j] = fmaf(dy, r.x, dDv[j]);
+                    if constexpr (GATE) y[i][j] = r.dz * fmaf(Dv[j], r.x, y[i][j]);
+                }
+            const int64_t out = (r0 + tile * T) * D * E;
+            char *dxp = static_cast<char*>(ka->dx) + out, *ddp = static_cast<char*>(ka->ddt) + out;
+            char* dzp = GATE ? static_cast<char*>(ka->dz) + out : nullptr;
+            const uint32_t ds = static_cast<uint32_t>(D) * E;
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const SelRaw<T_, TY> r = raw[t][j][lane];
-                const float x = static_cast<float>(r.x), v = static_cast<float>(r.dt) + dtp[j].bias;
-                float gB = 0.f, gA = 0.f, y = Dv[j] * x;
+                const uint32_t o = static_cast<uint32_t>(c[j]) * E;
+                auto store = [&](int i) {
+                    const uint64_t t = static_cast<uint32_t>(w + W * i) * ds;
+                    *reinterpret_cast<T_*>(dxp + t + o) = static_cast<T_>(dx[i][j]);
+                    *reinterpret_cast<T_*>(ddp + t + o) = static_cast<T_>(dd[i][j]);
+                    if constexpr (GATE) *reinterpret_cast<T_*>(dzp + t + o) = static_cast<T_>(y[i][j]);
+                };
+                if (!ragged && last >= T - 1) {
 #pragma unroll
-                for (int u = 0; u < W; ++u) {
-                    const float2 pp = part[u][t][j][lane];
-                    gB += pp.x;
-                    gA += pp.y;
-                    if constexpr (GATE) y += ypart[u][t][j][lane];
-                }
-                const float dy = sdy[t][j][lane], dt = st[t][j][lane].x;
-                const float dx = fmaf(Dv[j], dy, dt * gB);
-                float dd = fmaf(gA, 1.f / kLog2e, x * gB);
-                if (dtp[j].lo < dtp[j].hi) {
-                    const float u = dtp[j].softplus ? sel_softplus(v) : v;
-                    if (!(u >= dtp[j].lo && u <= dtp[j].hi)) dd = 0.f;
-                }
-                if (dtp[j].softplus) dd *= __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * kLog2e));
-                if (!ok[j]) dd = 0.f;
-                dbv[j] += dd;
-                dDv[j] = fmaf(dy, x, dDv[j]);
-                float dz = 0.f;
-                if constexpr (GATE) {
-                    const float z = static_cast<float>(r.z);
-                    const float sg = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * kLog2e));
-                    dz = static_cast<float>(r.dout) * y * sg * fmaf(z, 1.f - sg, 1.f);
-                }
-                if (ok[j]) {
-                    (static_cast<T_*>(a.dx) + out)[c[j]] = static_cast<T_>(dx);
-                    (static_cast<T_*>(a.ddt) + out)[c[j]] = static_cast<T_>(dd);
-                    if constexpr (GATE) (static_cast<T_*>(a.dz) + out)[c[j]] = static_cast<T_>(dz);
+                    for (int i = 0; i < TPT; ++i) store(i);
+                } else if (ok[j]) {
+#pragma unroll
+                    for (int i = 0; i < TPT; ++i)
+                        if (w + W * i <= last) store(i);
                 }
             }
         }
-        if (tile > 0) rows[0].template load<true>(row_of(a.B, tile - 1), row_of(a.C, tile - 1), bs, 0, T - 1);
+        if (tile > 0) rows[0].template load<true>(row_of(ka->B, tile - 1), row_of(ka->C, tile - 1), bs, 0, T - 1);
         __syncthreads();
     }
     const int64_t bc = b * lay.chunks + chunk;
