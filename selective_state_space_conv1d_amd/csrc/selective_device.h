@@ -47,9 +47,11 @@ __device__ __forceinline__ float sel_dt(float v, const SelDt& p) {
 typedef const uint32_t __attribute__((address_space(4))) ScalarWord;
 typedef const char __attribute__((address_space(4))) ScalarByte;
 template <typename T, int S>
+constexpr int kRowWords = S * static_cast<int>(sizeof(T)) / 4;
+template <typename T, int S, int n_ = (kRowWords<T, S> >= 8 ? 1 : 8 / kRowWords<T, S>)>
 struct SelRows {
-    static constexpr int kWords = S * static_cast<int>(sizeof(T)) / 4;   // of one row
-    static constexpr int n = kWords >= 8 ? 1 : 8 / kWords;
+    static constexpr int kWords = kRowWords<T, S>;
+    static constexpr int n = n_;
     uint32_t bw[n][kWords], cw[n][kWords];
     template <bool WITH_C>
     __device__ __forceinline__ void load(const char* b, const char* c, uint32_t stride, int first, int last) {
@@ -64,6 +66,13 @@ struct SelRows {
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) cw[t][i] = q[i];
         }
+    }
+    // keeps the values as loaded: widened ones from before are not held on to
+    __device__ __forceinline__ void renew() {
+#pragma unroll
+        for (int t = 0; t < n; ++t)
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) asm volatile("" : "+s"(bw[t][i]), "+s"(cw[t][i]));
     }
     static __device__ __forceinline__ float value(const uint32_t* w, int s) {
         if constexpr (sizeof(T) == 2) return __uint_as_float(s & 1 ? w[s / 2] & 0xffff0000u : w[s / 2] << 16);

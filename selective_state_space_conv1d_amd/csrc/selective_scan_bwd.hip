@@ -256,8 +256,9 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
     typedef SelGradShape<N> Z;
     constexpr int S = Z::S, W = Z::W, T = Z::T, P = Z::CPL, E = sizeof(T_);
     constexpr int TPT = (T + W - 1) / W, M = S * T / 16;
-    constexpr int SUB = SelRows<T_, S>::n < T ? SelRows<T_, S>::n : T;
-    constexpr int K = T / SUB;              // sub-tiles whose B and C are in scalar registers
+    // sub-tiles whose B and C are in scalar registers: the whole tile where it takes 32 of them
+    constexpr int SUB = 2 * T * kRowWords<T_, S> <= 32 ? T : SelRows<T_, S>::n;
+    constexpr int K = T / SUB;
     __shared__ float2 st[T][P][64];         // dt, dt * x
     __shared__ float sdy[T][P][64];         // dy
     __shared__ float2 part[W][T][P][64];    // <g, B>, <g q, A2> over the wave's states
@@ -355,7 +356,7 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
     auto row_of = [&](const void* p, int tile) {   // this wave's states of the tile's first row of B or C
         return static_cast<const char*>(p) + ((r0 + tile * T) * a.bc_row_stride + grp * N + w * S) * E;
     };
-    SelRows<T_, S> rows[2];
+    SelRows<T_, S, SUB> rows[2];
     if (tiles > 0) {
         load(tiles - 1);
         load_state(tiles - 1);
@@ -423,18 +424,25 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
                 for (int s = 0; s < S; ++s) h[j][s] = fmaf(__builtin_amdgcn_exp2f(ts[j] * A2[j][s]), hin[j][s], h[j][s]);
         __syncthreads();
         float q[T][P][S], ea[T][P][S];
+        float2 dn[2][P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) dn[0][j] = st[0][j][lane];
 #pragma unroll
         for (int u = 0; u < K; ++u) {
             const int at = u & 1;
             // the way back starts with the last rows of the way forward
             if (u + 1 < K) rows[at ^ 1].template load<true>(Bp, Cp, bs, (u + 1) * SUB, last);
-            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int v = 0; v < SUB; ++v) {
                 const int t = u * SUB + v;
+                // dt and dt x are read from LDS a token ahead
+                if (t + 1 < T)
+#pragma unroll
+                    for (int j = 0; j < P; ++j) dn[(t + 1) & 1][j] = st[t + 1][j][lane];
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
-                    const float2 d = st[t][j][lane];
+                    const float2 d = dn[t & 1][j];
                     float y = 0.f;
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
@@ -450,6 +458,10 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
         // the next tile's loads; h is free from here on
         load(tile > 0 ? tile - 1 : 0);
         load_state(tile > 0 ? tile - 1 : 0);
+        float yn[2][P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) yn[(T - 1) & 1][j] = sdy[T - 1][j][lane];
+        rows[(K - 1) & 1].renew();
         f32x4 accB[M], accC[M];
         int col = lane & 15;
         asm volatile("" : "+v"(col));   // the one-hot operands are made where they are used: kept, they spill
@@ -459,15 +471,21 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
         for (int u = K - 1; u >= 0; --u) {
             const int at = u & 1;
             if (u > 0) rows[at ^ 1].template load<true>(Bp, Cp, bs, (u - 1) * SUB, last);
-            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int v = SUB - 1; v >= 0; --v) {
                 const int t = u * SUB + v;
+                if (t > 0)
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        dn[(t - 1) & 1][j] = st[t - 1][j][lane];
+                        yn[(t - 1) & 1][j] = sdy[t - 1][j][lane];
+                    }
+                __builtin_amdgcn_sched_barrier(0);
                 float pB[S], pC[S];
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
-                    const float2 d = st[t][j][lane];
-                    const float dy = sdy[t][j][lane];
+                    const float2 d = dn[t & 1][j];
+                    const float dy = yn[t & 1][j];
                     float gB = 0.f, gA = 0.f;
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
