@@ -601,8 +601,7 @@ ssd_status_t ssd_selective_scan(const ssd_dims_t* d, const void* x, int64_t x_ro
  *  dA [D, N], dDskip [D], ddt_bias [D], dinit_state [B, D, N]: fp32; dDskip, ddt_bias and dinit_state
  *                may be NULL (not written).
  * Every gradient is overwritten, and is the same bit for bit on every call with the same inputs.
- * Sums over tokens and channels are fp32.  A dB or dC term that is not finite spreads within its block
- * of 16 (token, state) pairs.  The rest is as for ssd_selective_scan; a workspace of
+ * Sums over tokens and channels are fp32.  The rest is as for ssd_selective_scan; a workspace of
  * ssd_selective_scan_bwd_workspace_size() bytes is required.
  */
 size_t ssd_selective_scan_bwd_workspace_size(const ssd_dims_t* d);

@@ -14,12 +14,12 @@
 // first derives the chunk's true state and gradient at its ends from those of the other chunks.
 //
 // The layout is the forward's: lane = channel (CPL of them, 64 apart), wave = S of the N states.  Sums
-// over states stay in the lane; sums over channels (dB, dC: one value of each per token and state from
-// 64 lanes) would cost more vector operations than everything else, so the matrix pipe takes them: with
-// the values as the 16x4 operand and a one-hot 4x16 operand, v_mfma_f32_16x16x4_f32 adds lanes 16
-// apart into the column the one-hot names, in fp32; a tile's T S (token, state) pairs fill T S / 16
-// accumulators, whose rows are then added by 3 additions and half-wave and row exchanges.  (A product
-// that is not finite makes the other tokens of its tile non-finite too: 0 times infinity.)
+// over states stay in the lane.  Sums over channels (dB, dC: one value of each per token and state from
+// 64 lanes) are made of two sums at a time: a level adds lanes a power of two apart in both and leaves
+// one in the lanes whose bit is clear, the other in those where it is set, so that after six levels a
+// register holds 64 finished sums, at 2.2 vector operations for each value summed.  (The fp32 matrix
+// instruction against a one-hot operand takes fewer instructions, but holds the vector pipe for all of
+// its 32 cycles: 544 us for the gradients launch at 4 x 2048 x 4096 channels.)
 #include "selective_device.h"
 
 namespace ssd {
@@ -83,16 +83,37 @@ static SelBwdLayout bwd_layout(int64_t batch, int64_t L, int64_t D, int64_t G, i
     }
 }
 
-// The sum over the two half waves of x in the lower half of the result, that of y in the upper.
-__device__ __forceinline__ float add_halves(float x, float y) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+// Level LEVEL of the lane sums: adds lanes 2^(5 - LEVEL) apart of a and of b; a's sums are left in the
+// lanes whose bit 5 - LEVEL is clear, b's in the others.
+template <int LEVEL>
+__device__ __forceinline__ float merge_sums(float a, float b, int lane) {
+    if constexpr (LEVEL == 0) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    } else if constexpr (LEVEL == 1) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    } else {
+        // row_ror:8, row_half_mirror, quad_perm [2,3,0,1], quad_perm [1,0,3,2]: the mirror pairs other lanes
+        // than 4 apart, but each of one half of the eight with one of the other, which is what the sum needs
+        constexpr int ctrl = LEVEL == 2 ? 0x128 : LEVEL == 3 ? 0x141 : LEVEL == 4 ? 0x4E : 0xB1;
+        const float x = a + dpp_f<ctrl, 0xF>(a), y = b + dpp_f<ctrl, 0xF>(b);
+        return (lane >> (5 - LEVEL)) & 1 ? y : x;
+    }
 }
-// In each half wave, the sum over the two rows of 16 lanes of x in the first row, that of y in the second.
-__device__ __forceinline__ float add_rows(float x, float y) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+// Levels FROM, FROM + 1, ... over K registers, until one is left.
+template <int FROM, int K>
+__device__ __forceinline__ float merge_all(const float (&v)[K], int lane) {
+    if constexpr (K == 1) {
+        return v[0];
+    } else {
+        float r[K / 2];
+#pragma unroll
+        for (int i = 0; i < K / 2; ++i) r[i] = merge_sums<FROM>(v[2 * i], v[2 * i + 1], lane);
+        return merge_all<FROM + 1>(r, lane);
+    }
 }
+constexpr int ilog2(int n) { return n <= 1 ? 0 : 1 + ilog2(n / 2); }
 
 // (1) SPLIT: chunks from a zero state, with the sums of dt and the gradients at their starts.
 template <typename T_, typename TY, int S, int W, int T, bool SPLIT, bool GATE>
@@ -255,7 +276,9 @@ template <typename T_, typename TY, int N, bool SPLIT, bool GATE>
 __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_kernel(SelBwdArgs a, float* ws, SelBwdLayout lay) {
     typedef SelGradShape<N> Z;
     constexpr int S = Z::S, W = Z::W, T = Z::T, P = Z::CPL, E = sizeof(T_);
-    constexpr int TPT = (T + W - 1) / W, M = S * T / 16;
+    constexpr int TPT = (T + W - 1) / W;
+    // levels of the lane sums over a token's 2 S values, tokens that share a register of finished sums
+    constexpr int LV = ilog2(2 * S), TG = 64 / (2 * S);
     // sub-tiles whose B and C are in scalar registers: the whole tile where it takes 32 of them
     constexpr int SUB = 2 * T * kRowWords<T_, S> <= 32 ? T : SelRows<T_, S>::n;
     constexpr int K = T / SUB;
@@ -462,11 +485,7 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
 #pragma unroll
         for (int j = 0; j < P; ++j) yn[(T - 1) & 1][j] = sdy[T - 1][j][lane];
         rows[(K - 1) & 1].renew();
-        f32x4 accB[M], accC[M];
-        int col = lane & 15;
-        asm volatile("" : "+v"(col));   // the one-hot operands are made where they are used: kept, they spill
-#pragma unroll
-        for (int m = 0; m < M; ++m) accB[m] = accC[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float tok[T];
 #pragma unroll
         for (int u = K - 1; u >= 0; --u) {
             const int at = u & 1;
@@ -501,13 +520,13 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
                     }
                     part[w][t][j][lane] = make_float2(gB, gA);
                 }
+                float vals[2 * S];
 #pragma unroll
                 for (int s = 0; s < S; ++s) {
-                    const int f = s * T + t;   // the pair's place: accumulator f / 16, column f % 16
-                    const float hot = col == (f & 15) ? 1.f : 0.f;
-                    accB[f >> 4] = __builtin_amdgcn_mfma_f32_16x16x4f32(pB[s], hot, accB[f >> 4], 0, 0, 0);
-                    accC[f >> 4] = __builtin_amdgcn_mfma_f32_16x16x4f32(pC[s], hot, accC[f >> 4], 0, 0, 0);
+                    vals[s] = pB[s];
+                    vals[S + s] = pC[s];
                 }
+                tok[t] = merge_all<0>(vals, lane);
             }
         }
         // dA's products are added here and not, as the compiler would have it, after the next barrier
@@ -515,22 +534,17 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
         for (int j = 0; j < P; ++j)
 #pragma unroll
             for (int s = 0; s < S; ++s) asm volatile("" : "+v"(dA[j][s]));
-        // Rows of the accumulators: 4 in the lane; the other sums by exchanging half waves and rows
-        // between two sums at a time, which leaves four pairs' sums in the four rows of one register.
+        // lane bits 5, 4, ...: the value's bits 0, 1, ... (dB's S states, then dC's), then the token's
         float* bcp = ws + lay.dBC + (static_cast<int64_t>(blk) * a.batch * a.seqlen + r0 + tile * T) * 2 * N + w * S;
-        float sums[2 * M];
+        const int rev = static_cast<int>(__brev(static_cast<uint32_t>(lane)) >> 26), val = rev & (2 * S - 1), tt = rev >> LV;
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-            sums[m] = (accB[m][0] + accB[m][1]) + (accB[m][2] + accB[m][3]);
-            sums[M + m] = (accC[m][0] + accC[m][1]) + (accC[m][2] + accC[m][3]);
-        }
+        for (int g = 0; g < T / TG; ++g) {
+            float group[TG];
 #pragma unroll
-        for (int m = 0; m < 2 * M; m += 4) {
-            const float v = add_rows(add_halves(sums[m], sums[m + 1]), add_halves(sums[m + 2], sums[m + 3]));
-            // row 0: sum m, row 1: m + 2, row 2: m + 1, row 3: m + 3
-            const int row = lane >> 4, mm = m + (row == 1 ? 2 : row == 2 ? 1 : row);
-            const int f = (mm % M) * 16 + (lane & 15), t = f % T, s = f / T;
-            if (t <= last) bcp[static_cast<uint32_t>(t * 2 * N + mm / M * N + s)] = v;
+            for (int i = 0; i < TG; ++i) group[i] = tok[g * TG + i];
+            const float v = merge_all<LV>(group, lane);
+            const int t = g * TG + tt;
+            if (t <= last) bcp[static_cast<uint32_t>(t * 2 * N + val / S * N + val % S)] = v;
         }
         __syncthreads();
         const SelBwdArgsPtr ka = reread_args();
