@@ -4,23 +4,29 @@
 // The states' own gradients: conv_state_out[k] = u~[L-4+k] adds to du~, and conv_state_in's gradient is
 // du~ at the four positions before the first token (the oldest feeds no output).
 //
-// A thread owns one 16-byte vector of channels and walks a tile of tokens with the last three inputs
+// A thread owns four channels (eight of bf16 would take more registers than two waves a SIMD have) and walks a tile of tokens with the last three inputs
 // and q values in registers, so each input is read once (plus three rows on either side of a tile) and
-// each output written once: bound by HBM.  dw and dbias are summed in registers over the tile, over
-// the workgroup's tiles in LDS and over workgroups by a second launch, in a fixed order.
+// each output written once: bound by HBM.  Rows are taken four at a time, the next four loaded while
+// four are computed.  dw and dbias are summed in registers over the tile, over the workgroup's tiles
+// in LDS and over workgroups by a second launch, in a fixed order.
 #include "ssd_device.h"
 #include "ssd_kernels.h"
 
+#include <type_traits>
+
 namespace ssd {
 
-constexpr int kCbLanes = 64;     // channel vectors per workgroup
-constexpr int kCbSub = 4;        // token tiles per workgroup, one for each wave
-constexpr int kCbTokens = 64;    // tokens per tile
+constexpr int kCbV = 4;           // channels per thread
+constexpr int kCbLanes = 64;      // threads across the channels of a workgroup
+constexpr int kCbSub = 4;         // token tiles per workgroup, one for each wave
+constexpr int kCbSteps = 128;     // rows a tile walks: its tokens and the three after them
+constexpr int kCbTokens = kCbSteps - 3;
 
 template <typename T>
 __global__ __launch_bounds__(kCbLanes * kCbSub) void conv1d_bwd_kernel(ConvBwdArgs a, float* __restrict__ part,
                                                                        int64_t tblocks, int64_t cblocks) {
-    constexpr int V = Vec16<T>::n;
+    constexpr int V = kCbV;
+    typedef T Raw __attribute__((ext_vector_type(V)));
     __shared__ float red[kCbSub][5][V][kCbLanes];
     const int lane = threadIdx.x % kCbLanes, sub = threadIdx.x / kCbLanes;
     const int64_t cb = blockIdx.x % cblocks, tb = blockIdx.x / cblocks % tblocks, b = blockIdx.x / (cblocks * tblocks);
@@ -49,58 +55,84 @@ __global__ __launch_bounds__(kCbLanes * kCbSub) void conv1d_bwd_kernel(ConvBwdAr
     // du~[t] from outside the outputs: the stored windows
     auto stored = [&](int64_t t, int v) { return dso && t >= L - 4 ? static_cast<float>(dso[v * 4 + (t - L + 4)]) : 0.f; };
     if (ok && t0 < t1) {
-        float u0[V], u1[V], u2[V], q1[V], q2[V], q3[V];   // u~[t-3..t-1]; q[t-1], q[t-2], q[t-3]
-        auto input = [&](int64_t t, float (&o)[V]) {
-            if (t >= 0) load16_f32(xp + t * a.xbc_row_stride, o);
-            else
+        float u[7][V], q[7][V];     // u~ and q of tokens t-3 .. t+3
+        Raw nu[4], ng[4];           // input and output gradient of the next four tokens, as loaded
+        auto load = [&](int64_t t) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) o[v] = sin ? static_cast<float>(sin[v * 4 + 4 + t]) : 0.f;
-        };
-        input(t0 - 3, u0);
-        input(t0 - 2, u1);
-        input(t0 - 1, u2);
-#pragma unroll
-        for (int v = 0; v < V; ++v) q1[v] = q2[v] = q3[v] = 0.f;
-        // q of three tokens past the tile are needed for its last inputs; past L they are 0
-        for (int64_t t = t0; t < t1 + 3; ++t) {
-            float u3[V], go[V], q[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) u3[v] = go[v] = 0.f;
-            if (t < L) {
-                load16_f32(xp + t * a.xbc_row_stride, u3);
-                load16_f32(gp + t * CD, go);
+            for (int r = 0; r < 4; ++r) {
+                const int64_t row = t + r < L ? t + r : L - 1;
+                nu[r] = __builtin_nontemporal_load(reinterpret_cast<const Raw*>(xp + row * a.xbc_row_stride));
+                ng[r] = __builtin_nontemporal_load(reinterpret_cast<const Raw*>(gp + row * CD));
             }
-            float du[V];
+        };
+        load(t0);
+#pragma unroll
+        for (int r = 0; r < 3; ++r) {
+            const int64_t t = t0 - 3 + r;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float p = fmaf(wt[3][v], u3[v], fmaf(wt[2][v], u2[v], fmaf(wt[1][v], u1[v], fmaf(wt[0][v], u0[v], bs[v]))));
-                const float sg = __builtin_amdgcn_rcpf(1.f + __expf(-p));
-                q[v] = t < L ? go[v] * sg * fmaf(p, 1.f - sg, 1.f) : 0.f;
-                if (t < t1) {
-                    dw[0][v] = fmaf(q[v], u0[v], dw[0][v]);
-                    dw[1][v] = fmaf(q[v], u1[v], dw[1][v]);
-                    dw[2][v] = fmaf(q[v], u2[v], dw[2][v]);
-                    dw[3][v] = fmaf(q[v], u3[v], dw[3][v]);
-                    db[v] += q[v];
-                }
-                du[v] = fmaf(wt[3][v], q3[v], fmaf(wt[2][v], q2[v], fmaf(wt[1][v], q1[v], wt[0][v] * q[v])));
-                u0[v] = u1[v];
-                u1[v] = u2[v];
-                u2[v] = u3[v];
-                q3[v] = q2[v];
-                q2[v] = q1[v];
-                q1[v] = q[v];
+                u[r][v] = t >= 0 ? static_cast<float>(xp[t * a.xbc_row_stride + v]) : sin ? static_cast<float>(sin[v * 4 + 4 + t]) : 0.f;
+                q[r][v] = 0.f;
             }
-            // du belongs to token t - 3; before the tile's first token the earlier tile owns it, and
-            // before the sequence's first it is the conv state's
-            const int64_t r = t - 3;
-            if (dso && r >= L - 4)
+        }
+        // rows t .. t+3: q there, then du~ of rows t-3 .. t, whose last q is now known.  EDGE: some of
+        // them before the tile or its sequence, after the tile or in the last windows.
+        auto rows = [&](int64_t t, auto edge) {
+            constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll
-                for (int v = 0; v < V; ++v) du[v] += stored(r, v);
-            if (r >= t0) store16_f32(dp + r * CD, du);
-            else if (t0 == 0 && dsi)
+            for (int r = 0; r < 4; ++r) {
+                const bool in = !EDGE || t + r < L, own = !EDGE || t + r < t1;
 #pragma unroll
-                for (int v = 0; v < V; ++v) dsi[v * 4 + 4 + r] = static_cast<T>(du[v]);
+                for (int v = 0; v < V; ++v) {
+                    const float p = fmaf(wt[3][v], u[r + 3][v], fmaf(wt[2][v], u[r + 2][v], fmaf(wt[1][v], u[r + 1][v], fmaf(wt[0][v], u[r][v], bs[v]))));
+                    const float sg = __builtin_amdgcn_rcpf(1.f + __expf(-p));
+                    // past the sequence's end there is no output
+                    q[r + 3][v] = in ? q[r + 3][v] * sg * fmaf(p, 1.f - sg, 1.f) : 0.f;
+                    if (own) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) dw[k][v] = fmaf(q[r + 3][v], u[r + k][v], dw[k][v]);
+                        db[v] += q[r + 3][v];
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int64_t at = t - 3 + r;
+                float du[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    du[v] = fmaf(wt[3][v], q[r][v], fmaf(wt[2][v], q[r + 1][v], fmaf(wt[1][v], q[r + 2][v], wt[0][v] * q[r + 3][v])));
+                    if (EDGE && dso && at >= L - 4 && at < L) du[v] += stored(at, v);
+                }
+                if (!EDGE || (at >= t0 && at < t1)) {
+                    Raw o;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) o[v] = static_cast<T>(du[v]);
+                    __builtin_nontemporal_store(o, reinterpret_cast<Raw*>(dp + at * CD));
+                } else if (t0 == 0 && at < 0 && dsi) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) dsi[v * 4 + 4 + at] = static_cast<T>(du[v]);
+                }
+            }
+        };
+        for (int64_t t = t0; t < t1 + 3; t += 4) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    u[r + 3][v] = static_cast<float>(nu[r][v]);
+                    q[r + 3][v] = static_cast<float>(ng[r][v]);
+                }
+            load(t + 4);
+            if (t > t0 && t + 3 < t1 && t + 4 < L) rows(t, std::false_type{});
+            else rows(t, std::true_type{});
+#pragma unroll
+            for (int r = 0; r < 3; ++r)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    u[r][v] = u[r + 4][v];
+                    q[r][v] = q[r + 4][v];
+                }
         }
         if (t0 == 0 && dsi)
 #pragma unroll
@@ -153,7 +185,7 @@ size_t conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t channel
 
 template <typename T>
 static hipError_t conv_bwd_t(const ConvBwdArgs& a, float* part, hipStream_t s) {
-    constexpr int V = Vec16<T>::n;
+    constexpr int V = kCbV;
     const int64_t tb = token_blocks(a.seqlen), cb = (a.channels + kCbLanes * V - 1) / (kCbLanes * V);
     const int64_t blocks = a.batch * tb * cb;
     if (blocks > 0)

@@ -806,7 +806,7 @@ ssd_status_t ssd_conv1d_bwd(const ssd_dims_t* d, const void* xbc, int64_t xbc_ro
     const bool tokens = d->batch > 0 && d->seqlen > 0;
     if (!dw || (tokens && (!xbc || !w || !dout || !dxbc))) return SSD_ERR_NULL;
     if (CD % 8 != 0) return SSD_ERR_UNSUPPORTED;
-    // workgroups (512 channels or fewer x 256 tokens) below 2^31
+    // workgroups (256 channels x 256 tokens or more) below 2^31
     if (d->batch > INT32_MAX || d->seqlen > INT32_MAX ||
         (d->batch > 0 && (d->seqlen / 256 + 1) * (CD / 256 + 1) > INT32_MAX / d->batch)) return SSD_ERR_UNSUPPORTED;
     if (tokens && xbc_row_stride < CD) return SSD_ERR_SHAPE;
