@@ -19,12 +19,20 @@ namespace ssd {
 constexpr int kCbV = 4;           // channels per thread
 constexpr int kCbLanes = 64;      // threads across the channels of a workgroup
 constexpr int kCbSub = 4;         // token tiles per workgroup, one for each wave
-constexpr int kCbSteps = 128;     // rows a tile walks: its tokens and the three after them
-constexpr int kCbTokens = kCbSteps - 3;
+
+// Rows that a tile walks, its tokens and the three after them: 128, fewer where that gives less than two
+// workgroups a CU (2 x 8192 x 18432, bf16: 408 us with 128, 440 with 64, 422 with 256; 1 x 8192 x 18432: 204,
+// 207, 241).
+static int64_t tile_steps(int64_t batch, int64_t L, int64_t CD) {
+    const int64_t cb = (CD + kCbLanes * kCbV - 1) / (kCbLanes * kCbV);
+    int64_t steps = 128;
+    while (steps > 16 && batch * cb * ((L + (steps - 3) * kCbSub - 1) / ((steps - 3) * kCbSub)) < 512) steps /= 2;
+    return steps;
+}
 
 template <typename T>
 __global__ __launch_bounds__(kCbLanes * kCbSub) void conv1d_bwd_kernel(ConvBwdArgs a, float* __restrict__ part,
-                                                                       int64_t tblocks, int64_t cblocks) {
+                                                                       int64_t tblocks, int64_t cblocks, int64_t tokens) {
     constexpr int V = kCbV;
     typedef T Raw __attribute__((ext_vector_type(V)));
     __shared__ float red[kCbSub][5][V][kCbLanes];
@@ -33,8 +41,8 @@ __global__ __launch_bounds__(kCbLanes * kCbSub) void conv1d_bwd_kernel(ConvBwdAr
     const int64_t CD = a.channels, L = a.seqlen;
     const bool ok = (cb * kCbLanes + lane) * V < CD;
     const int64_t c0 = ok ? (cb * kCbLanes + lane) * V : 0;
-    const int64_t t0 = (tb * kCbSub + sub) * kCbTokens;
-    const int64_t t1 = t0 + kCbTokens < L ? t0 + kCbTokens : L;
+    const int64_t t0 = (tb * kCbSub + sub) * tokens;
+    const int64_t t1 = t0 + tokens < L ? t0 + tokens : L;
     const T* xp = static_cast<const T*>(a.xbc) + b * L * a.xbc_row_stride + c0;
     const T* gp = static_cast<const T*>(a.dout) + b * L * CD + c0;
     T* dp = static_cast<T*>(a.dxbc) + b * L * CD + c0;
@@ -177,19 +185,20 @@ __global__ __launch_bounds__(256) void conv1d_bwd_state_kernel(const T* __restri
     if (i < n) dsi[i] = dso ? dso[i] : static_cast<T>(0.f);
 }
 
-static int64_t token_blocks(int64_t L) { return (L + kCbTokens * kCbSub - 1) / (kCbTokens * kCbSub); }
+static int64_t token_blocks(int64_t L, int64_t tokens) { return (L + tokens * kCbSub - 1) / (tokens * kCbSub); }
 
-size_t conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t channels, Dt act) {
-    return static_cast<size_t>(batch * token_blocks(seqlen) * 5 * channels) * sizeof(float);
+size_t conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t channels) {
+    return static_cast<size_t>(batch * token_blocks(seqlen, tile_steps(batch, seqlen, channels) - 3) * 5 * channels) * sizeof(float);
 }
 
 template <typename T>
 static hipError_t conv_bwd_t(const ConvBwdArgs& a, float* part, hipStream_t s) {
     constexpr int V = kCbV;
-    const int64_t tb = token_blocks(a.seqlen), cb = (a.channels + kCbLanes * V - 1) / (kCbLanes * V);
+    const int64_t tokens = tile_steps(a.batch, a.seqlen, a.channels) - 3;
+    const int64_t tb = token_blocks(a.seqlen, tokens), cb = (a.channels + kCbLanes * V - 1) / (kCbLanes * V);
     const int64_t blocks = a.batch * tb * cb;
     if (blocks > 0)
-        hipLaunchKernelGGL((conv1d_bwd_kernel<T>), dim3(static_cast<uint32_t>(blocks)), dim3(kCbLanes * kCbSub), 0, s, a, part, tb, cb);
+        hipLaunchKernelGGL((conv1d_bwd_kernel<T>), dim3(static_cast<uint32_t>(blocks)), dim3(kCbLanes * kCbSub), 0, s, a, part, tb, cb, tokens);
     else if (a.batch > 0 && a.dstate_in) {
         const int64_t n = a.batch * a.channels * 4;
         hipLaunchKernelGGL((conv1d_bwd_state_kernel<T>), dim3(static_cast<uint32_t>((n + 255) / 256)), dim3(256), 0, s,

@@ -267,6 +267,12 @@ hipError_t launch_selective_scan(const SelScanArgs& a, Dt act, Dt ydt, void* wor
 constexpr int kSelUpdThreads = 256;
 constexpr int kUpdInFlight = 4;
 
+// Four consecutive values at any address that suits one of them.
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) Four {
+    T v[4];
+};
+
 template <typename T, typename TY, int N>
 __global__ __launch_bounds__(kSelUpdThreads) void selective_update_kernel(SelUpdateArgs a) {
     constexpr int Q = N / 4;
@@ -290,6 +296,8 @@ __global__ __launch_bounds__(kSelUpdThreads) void selective_update_kernel(SelUpd
     for (int64_t b0 = static_cast<int64_t>(blockIdx.y) * a.per_block; b0 < bend; b0 += kUpdInFlight) {
         f32x4 h[kUpdInFlight];
         int64_t slot[kUpdInFlight];
+        T xr[kUpdInFlight], dr[kUpdInFlight], zr[kUpdInFlight];
+        Four<T> Bv[kUpdInFlight], Cv[kUpdInFlight];
 #pragma unroll
         for (int i = 0; i < kUpdInFlight; ++i) {
             const int64_t b = b0 + i < bend ? b0 + i : bend - 1;
@@ -297,26 +305,29 @@ __global__ __launch_bounds__(kSelUpdThreads) void selective_update_kernel(SelUpd
             h[i] = slot[i] >= 0 ? __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(
                                       a.state + (slot[i] * D + c) * N + 4 * q))
                                 : f32x4{0.f, 0.f, 0.f, 0.f};
+            xr[i] = x[b * a.x_row_stride + c];
+            dr[i] = dt[b * D + c];
+            if (z) zr[i] = z[b * a.z_row_stride + c];
+            Bv[i] = *reinterpret_cast<const Four<T>*>(B + b * a.bc_row_stride + bo);
+            Cv[i] = *reinterpret_cast<const Four<T>*>(C + b * a.bc_row_stride + bo);
         }
 #pragma unroll
         for (int i = 0; i < kUpdInFlight; ++i) {
             const bool in = ok && b0 + i < bend;
             const int64_t b = b0 + i < bend ? b0 + i : bend - 1;
-            const float xv = static_cast<float>(x[b * a.x_row_stride + c]);
-            const float dv = sel_dt(static_cast<float>(dt[b * D + c]), dtp);
+            const float xv = static_cast<float>(xr[i]);
+            const float dv = sel_dt(static_cast<float>(dr[i]), dtp);
             const float dx = dv * xv, d2 = dv * kLog2e;
             float y = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float Bv = static_cast<float>(B[b * a.bc_row_stride + bo + k]);
-                const float Cv = static_cast<float>(C[b * a.bc_row_stride + bo + k]);
-                h[i][k] = fmaf(__builtin_amdgcn_exp2f(d2 * A4[k]), h[i][k], dx * Bv);
-                y = fmaf(h[i][k], Cv, y);
+                h[i][k] = fmaf(__builtin_amdgcn_exp2f(d2 * A4[k]), h[i][k], dx * static_cast<float>(Bv[i].v[k]));
+                y = fmaf(h[i][k], static_cast<float>(Cv[i].v[k]), y);
             }
             y = group_sum_last<Q>(y);   // every lane takes part: those past the end hold channel 0's values
             if (in && q == Q - 1) {
                 y = fmaf(Dv, xv, y);
-                if (z) y *= silu_f(static_cast<float>(z[b * a.z_row_stride + c]));
+                if (z) y *= silu_f(static_cast<float>(zr[i]));
                 static_cast<TY*>(a.y)[b * D + c] = static_cast<TY>(y);
             }
             if (in && slot[i] >= 0)

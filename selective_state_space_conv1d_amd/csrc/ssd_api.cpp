@@ -793,7 +793,7 @@ ssd_status_t ssd_selective_state_update(const ssd_dims_t* d, const float* state,
 
 size_t ssd_conv1d_bwd_workspace_size(const ssd_dims_t* d) {
     if (check_dims(d, true) != SSD_OK || d->batch > INT32_MAX || d->seqlen > INT32_MAX) return 0;
-    return ssd::conv1d_bwd_workspace_bytes(d->batch, d->seqlen, ssd_conv_dim(d), static_cast<Dt>(d->act_dtype));
+    return ssd::conv1d_bwd_workspace_bytes(d->batch, d->seqlen, ssd_conv_dim(d));
 }
 
 ssd_status_t ssd_conv1d_bwd(const ssd_dims_t* d, const void* xbc, int64_t xbc_row_stride, const void* w,
@@ -806,9 +806,9 @@ ssd_status_t ssd_conv1d_bwd(const ssd_dims_t* d, const void* xbc, int64_t xbc_ro
     const bool tokens = d->batch > 0 && d->seqlen > 0;
     if (!dw || (tokens && (!xbc || !w || !dout || !dxbc))) return SSD_ERR_NULL;
     if (CD % 8 != 0) return SSD_ERR_UNSUPPORTED;
-    // workgroups (256 channels x 256 tokens or more) below 2^31
+    // workgroups (256 channels x 52 tokens or more) below 2^31
     if (d->batch > INT32_MAX || d->seqlen > INT32_MAX ||
-        (d->batch > 0 && (d->seqlen / 256 + 1) * (CD / 256 + 1) > INT32_MAX / d->batch)) return SSD_ERR_UNSUPPORTED;
+        (d->batch > 0 && (d->seqlen / 52 + 1) * (CD / 256 + 1) > INT32_MAX / d->batch)) return SSD_ERR_UNSUPPORTED;
     if (tokens && xbc_row_stride < CD) return SSD_ERR_SHAPE;
     if (tokens && !stride_ok(xbc_row_stride, d->act_dtype)) return SSD_ERR_ALIGN;
     for (const void* p : {xbc, w, bias, conv_state_in, dout, dconv_state_out, static_cast<const void*>(dxbc),

@@ -198,7 +198,7 @@ struct PoolCopyArgs {
 };
 
 hipError_t launch_conv1d_fwd(const ConvFwdArgs& a, Dt act, hipStream_t s);
-size_t conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t channels, Dt act);
+size_t conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t channels);
 hipError_t launch_conv1d_bwd(const ConvBwdArgs& a, Dt act, void* workspace, hipStream_t s);
 size_t selective_scan_workspace_bytes(int64_t batch, int64_t seqlen, int channels, int ngroups, int d_state);
 hipError_t launch_selective_scan(const SelScanArgs& a, Dt act, Dt ydt, void* workspace, hipStream_t s);

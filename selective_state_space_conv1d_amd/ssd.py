@@ -1063,19 +1063,20 @@ def ssd_conv1d_update_accept(xbc, conv_state, accept_len, slot_idx=None, nheads=
 
 
 # --------------------------------------------------------------------------- per-channel selective scan
-class _On:
-    """Makes the tensors' device, and a given stream, current for the allocations and launches of one call.
-    The buffers that the call allocates then belong to the stream that uses them."""
+class _Nothing:
+    def __enter__(self):
+        pass
 
-    def __init__(self, dev, stream):
-        self.inner = []
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-            if stream != torch.cuda.current_stream(dev):
-                self.inner.append(torch.cuda.stream(stream))
-        elif dev.type == "cuda" and dev.index != torch.cuda.current_device():
-            self.inner.append(torch.cuda.device(dev))
+    def __exit__(self, *e):
+        pass
+
+
+_NOTHING = _Nothing()
+
+
+class _Within:
+    def __init__(self, inner):
+        self.inner = inner
 
     def __enter__(self):
         for c in self.inner:
@@ -1086,13 +1087,39 @@ class _On:
             c.__exit__(*e)
 
 
+def _on(dev, stream):
+    """Makes the tensors' device, and a given stream, current for the allocations and launches of one call.
+    The buffers that the call allocates then belong to the stream that uses them."""
+    if stream is None:
+        if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+            return _NOTHING
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return _Within([torch.cuda.device(dev), torch.cuda.stream(stream)])
+
+
+def _at(t):
+    """A tensor's address for the C ABI."""
+    return None if t is None else t.data_ptr()
+
+
+def _dense(t, name, dev, shape, dtype):
+    """_need for a contiguous tensor, with a short way for one that is as it should be."""
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        return t
+    return _need(t, name, dev, shape, dtype)
+
+
 def _workspace(size, workspace, dev):
     """(workspace tensor or None, its bytes): the caller's, or one allocated to the size the call needs."""
     if workspace is None:
         if size == 0:
             return None, 0
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", dev)
+    else:
+        _need(workspace, "workspace", dev)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -1100,52 +1127,60 @@ def _new(t, name, dev, shape, dtype):
     """The caller's output t, checked, or a new tensor."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    return _need(t, name, dev, shape, dtype)
+    return _dense(t, name, dev, shape, dtype)
+
+
+def _rows_of(t, name, dev, shape, dtype, lead, inner):
+    """The stride in elements between the token rows of t [*lead, ...], whose last axes (`inner` elements
+    together) must be packed and whose batch rows must be whole sequences apart."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == dev):
+        _need(t, name, dev, shape, dtype, contiguous=False)
+    Bt, L = lead if len(lead) == 2 else (1, lead[0])
+    if Bt * L == 0 or inner == 0:
+        return inner
+    st = t.stride()
+    size = 1
+    for n, s in zip(reversed(shape[len(lead):]), reversed(st)):
+        if n > 1 and s != size:
+            raise ValueError(f"{name} must have packed {'channels' if len(shape) == len(lead) + 1 else '(G, N)'}")
+        size *= n
+    if len(lead) == 1:
+        return st[0] if L > 1 else inner
+    if L == 1:
+        return st[0] if Bt > 1 else inner
+    if Bt > 1 and st[0] != L * st[1]:
+        raise ValueError(f"{name} must have a uniform token stride")
+    return st[1]
 
 
 def _selective_args(x, dt, A, B, C, D, z, dt_bias, rows):
     """Checks the inputs that every per-channel call has, x with `rows` leading axes (2: [B, L, D],
     1: [B, D]); returns (device, D, G, N, strides of x, of B and C, of z)."""
     dev = _device(x, "x")
-    if x.dim() != rows + 1:
+    shape, dtype = tuple(x.shape), x.dtype
+    if len(shape) != rows + 1:
         raise ValueError(f"x must have {rows + 1} axes")
-    lead, Dc = tuple(x.shape[:-1]), x.shape[-1]
-    if x.dtype not in _DT:
-        raise ValueError(f"activations must be float32 or bfloat16 (got {x.dtype})")
-    L = lead[1] if rows == 2 else 1
-    empty = x.numel() == 0
-    for t, nm in ((x, "x"), (z, "z")):
-        if t is None:
-            continue
-        _need(t, nm, dev, lead + (Dc,), x.dtype, contiguous=False)
-        if not empty and ((t.stride(-1) != 1 and Dc > 1) or (L > 1 and not _uniform_rows(t, L))):
-            raise ValueError(f"{nm} must have packed channels and a uniform token stride")
+    lead, Dc = shape[:-1], shape[-1]
+    if dtype not in _DT:
+        raise ValueError(f"activations must be float32 or bfloat16 (got {dtype})")
     _need(A, "A", dev, dtype=torch.float32)
     if A.dim() != 2 or A.shape[0] != Dc:
         raise ValueError(f"A must be [{Dc}, N]")
     N = A.shape[1]
-    _need(B, "B", dev, dtype=x.dtype, contiguous=False)
-    if B.dim() != rows + 2 or tuple(B.shape[:-2]) != lead or B.shape[-1] != N:
-        raise ValueError(f"B must have shape {lead + ('G', N)} (got {tuple(B.shape)})")
+    if not isinstance(B, torch.Tensor) or B.dim() != rows + 2:
+        raise ValueError(f"B must be a tensor of {rows + 2} axes")
     G = B.shape[-2]
     if G == 0 or Dc % G:
         raise ValueError(f"the channels ({Dc}) must be a multiple of B's groups ({G})")
-    _need(C, "C", dev, tuple(B.shape), x.dtype, contiguous=False)
-    for t, nm in ((B, "B"), (C, "C")):
-        if not empty and (t.stride(-1) != 1 or (G > 1 and t.stride(-2) != N) or (L > 1 and not _uniform_rows(t, L))):
-            raise ValueError(f"{nm} must have packed (G, N) and a uniform token stride")
-    one = rows == 2 and lead[0] * L <= 1 or rows == 1 and lead[0] <= 1      # one row: its stride does not matter
-    tok = rows - 1 if rows == 1 or L > 1 else 0                             # the axis whose stride parts rows
-    if not empty and not one and B.stride(tok) != C.stride(tok):
+    xs = _rows_of(x, "x", dev, shape, dtype, lead, Dc)
+    zs = Dc if z is None else _rows_of(z, "z", dev, shape, dtype, lead, Dc)
+    bcs = _rows_of(B, "B", dev, lead + (G, N), dtype, lead, G * N)
+    if _rows_of(C, "C", dev, lead + (G, N), dtype, lead, G * N) != bcs:
         raise ValueError("B and C must share a token stride")
-    _need(dt, "dt", dev, lead + (Dc,), x.dtype)
-    _need(D, "D", dev, (Dc,), torch.float32, optional=True)
-    _need(dt_bias, "dt_bias", dev, (Dc,), torch.float32, optional=True)
-
-    def stride(t, least):
-        return least if t is None or empty or one else t.stride(tok)
-
-    return dev, Dc, G, N, stride(x, Dc), stride(B, G * N), stride(z, Dc)
+    _dense(dt, "dt", dev, shape, dtype)
+    D is None or _dense(D, "D", dev, (Dc,), torch.float32)
+    dt_bias is None or _dense(dt_bias, "dt_bias", dev, (Dc,), torch.float32)
+    return dev, Dc, G, N, xs, bcs, zs
 
 
 def ssd_selective_scan(x, dt, A, B, C, D=None, z=None, init_state=None, final_state=None, y=None, y_dtype=None,
@@ -1157,16 +1192,16 @@ def ssd_selective_scan(x, dt, A, B, C, D=None, z=None, init_state=None, final_st
     N 16, 32, 64 or 128.  Returns y [B, L, D] in y_dtype (default x's)."""
     dev, Dc, G, N, xs, bcs, zs = _selective_args(x, dt, A, B, C, D, z, dt_bias, 2)
     Bt, L = x.shape[:2]
-    _need(init_state, "init_state", dev, (Bt, Dc, N), torch.float32, optional=True)
-    _need(final_state, "final_state", dev, (Bt, Dc, N), torch.float32, optional=True)
-    with _On(dev, stream):
+    init_state is None or _dense(init_state, "init_state", dev, (Bt, Dc, N), torch.float32)
+    final_state is None or _dense(final_state, "final_state", dev, (Bt, Dc, N), torch.float32)
+    with _on(dev, stream):
         ydt = y_dtype or (x.dtype if y is None else y.dtype)
         y = _new(y, "y", dev, (Bt, L, Dc), ydt)
         d = _dims(Bt, L, Dc, 1, G, N, x.dtype, ydt)
         workspace, ws = _workspace(int(_lib().ssd_selective_scan_workspace_size(ctypes.byref(d))), workspace, dev)
-        _check(_lib().ssd_selective_scan(ctypes.byref(d), _ptr(x), xs, _ptr(dt), _ptr(A), _ptr(B), _ptr(C), bcs, _ptr(D),
-                                         _ptr(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit), _ptr(init_state),
-                                         _ptr(final_state), _ptr(y), _ptr(workspace), ws, _stream(stream)),
+        _check(_lib().ssd_selective_scan(ctypes.byref(d), _at(x), xs, _at(dt), _at(A), _at(B), _at(C), bcs, _at(D),
+                                         _at(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit), _at(init_state),
+                                         _at(final_state), _at(y), _at(workspace), ws, _stream(stream)),
                "ssd_selective_scan")
     return y
 
@@ -1180,10 +1215,10 @@ def ssd_selective_scan_bwd(dy, x, dt, A, B, C, D=None, z=None, init_state=None, 
     dev, Dc, G, N, xs, bcs, zs = _selective_args(x, dt, A, B, C, D, z, dt_bias, 2)
     Bt, L = x.shape[:2]
     _need(dy, "dy", dev, (Bt, L, Dc))
-    _need(init_state, "init_state", dev, (Bt, Dc, N), torch.float32, optional=True)
-    _need(dfinal_state, "dfinal_state", dev, (Bt, Dc, N), torch.float32, optional=True)
+    init_state is None or _dense(init_state, "init_state", dev, (Bt, Dc, N), torch.float32)
+    dfinal_state is None or _dense(dfinal_state, "dfinal_state", dev, (Bt, Dc, N), torch.float32)
     d = _dims(Bt, L, Dc, 1, G, N, x.dtype, dy.dtype)
-    with _On(dev, stream):
+    with _on(dev, stream):
         def new(like, shape, dtype):
             return None if like is None else torch.empty(shape, dtype=dtype, device=dev)
 
@@ -1192,11 +1227,11 @@ def ssd_selective_scan_bwd(dy, x, dt, A, B, C, D=None, z=None, init_state=None, 
              "dz": new(z, x.shape, x.dtype), "ddt_bias": new(dt_bias, (Dc,), torch.float32),
              "dinit_state": new(init_state, (Bt, Dc, N), torch.float32)}
         workspace, ws = _workspace(int(_lib().ssd_selective_scan_bwd_workspace_size(ctypes.byref(d))), workspace, dev)
-        _check(_lib().ssd_selective_scan_bwd(ctypes.byref(d), _ptr(dy), _ptr(x), xs, _ptr(dt), _ptr(A), _ptr(B), _ptr(C),
-                                             bcs, _ptr(D), _ptr(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
-                                             _ptr(init_state), _ptr(dfinal_state), _ptr(o["dx"]), _ptr(o["ddt"]),
-                                             _ptr(o["dA"]), _ptr(o["dB"]), _ptr(o["dC"]), _ptr(o["dD"]), _ptr(o["dz"]),
-                                             _ptr(o["ddt_bias"]), _ptr(o["dinit_state"]), _ptr(workspace), ws,
+        _check(_lib().ssd_selective_scan_bwd(ctypes.byref(d), _at(dy), _at(x), xs, _at(dt), _at(A), _at(B), _at(C),
+                                             bcs, _at(D), _at(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
+                                             _at(init_state), _at(dfinal_state), _at(o["dx"]), _at(o["ddt"]),
+                                             _at(o["dA"]), _at(o["dB"]), _at(o["dC"]), _at(o["dD"]), _at(o["dz"]),
+                                             _at(o["ddt_bias"]), _at(o["dinit_state"]), _at(workspace), ws,
                                              _stream(stream)), "ssd_selective_scan_bwd")
     return o
 
@@ -1212,20 +1247,20 @@ def ssd_selective_state_update(state, x, dt, A, B, C, D=None, z=None, slot_idx=N
     _need(state, "state", dev, dtype=torch.float32)
     if state.dim() != 3 or tuple(state.shape[1:]) != (Dc, N):
         raise ValueError(f"state must be [B or nslots, {Dc}, {N}]")
-    _need(state_out, "state_out", dev, tuple(state.shape), torch.float32, optional=True)
+    state_out is None or _dense(state_out, "state_out", dev, tuple(state.shape), torch.float32)
     _need(slot_idx, "slot_idx", dev, optional=True)
     if state_out is not None and state_out.data_ptr() != state.data_ptr() and state.numel() > 0 and \
             abs(state_out.data_ptr() - state.data_ptr()) < 4 * state.numel():
         raise ValueError("state_out must be state or not overlap it")
     st, nslots, tab = _state_pool_args(state, slot_idx, Bt)
-    with _On(dev, stream):
+    with _on(dev, stream):
         ydt = y_dtype or (x.dtype if y is None else y.dtype)
         y = _new(y, "y", dev, (Bt, Dc), ydt)
         d = _dims(Bt, 1, Dc, 1, G, N, x.dtype, ydt)
-        _check(_lib().ssd_selective_state_update(ctypes.byref(d), _ptr(st), _ptr(st if state_out is None else state_out),
-                                                 _ptr(tab), nslots, _ptr(x), xs, _ptr(dt), _ptr(A), _ptr(B), _ptr(C), bcs,
-                                                 _ptr(D), _ptr(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
-                                                 _ptr(y), _stream(stream)), "ssd_selective_state_update")
+        _check(_lib().ssd_selective_state_update(ctypes.byref(d), _at(st), _at(st if state_out is None else state_out),
+                                                 _at(tab), nslots, _at(x), xs, _at(dt), _at(A), _at(B), _at(C), bcs,
+                                                 _at(D), _at(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
+                                                 _at(y), _stream(stream)), "ssd_selective_state_update")
     return y
 
 
@@ -1242,21 +1277,21 @@ def ssd_conv1d_bwd(dout, xbc, w, bias=None, conv_state_in=None, dconv_state_out=
         raise ValueError("xbc must be [B, L, CD] with packed channels and uniform token stride")
     H, P, G, N = _split_cd(CD, nheads, head_dim, ngroups, d_state)
     _conv_params(dev, CD, xbc.dtype, w, bias)
-    _need(dout, "dout", dev, (Bt, L, CD), xbc.dtype)
-    _need(conv_state_in, "conv_state_in", dev, (Bt, CD, 4), xbc.dtype, optional=True)
-    _need(dconv_state_out, "dconv_state_out", dev, (Bt, CD, 4), xbc.dtype, optional=True)
+    _dense(dout, "dout", dev, (Bt, L, CD), xbc.dtype)
+    conv_state_in is None or _dense(conv_state_in, "conv_state_in", dev, (Bt, CD, 4), xbc.dtype)
+    dconv_state_out is None or _dense(dconv_state_out, "dconv_state_out", dev, (Bt, CD, 4), xbc.dtype)
     d = _dims(Bt, L, H, P, G, N, xbc.dtype, xbc.dtype)
     xs = CD if Bt * L <= 1 else xbc.stride(1) if L > 1 else xbc.stride(0)
-    with _On(dev, stream):
+    with _on(dev, stream):
         def new(like, shape, dtype):
             return None if like is None else torch.empty(shape, dtype=dtype, device=dev)
 
         o = {"dxbc": new(xbc, (Bt, L, CD), xbc.dtype), "dw": new(w, (CD, 4), torch.float32),
              "dbias": new(bias, (CD,), torch.float32), "dconv_state_in": new(conv_state_in, (Bt, CD, 4), xbc.dtype)}
         workspace, ws = _workspace(int(_lib().ssd_conv1d_bwd_workspace_size(ctypes.byref(d))), workspace, dev)
-        _check(_lib().ssd_conv1d_bwd(ctypes.byref(d), _ptr(xbc), xs, _ptr(w), _ptr(bias), _ptr(conv_state_in), _ptr(dout),
-                                     _ptr(dconv_state_out), _ptr(o["dxbc"]), _ptr(o["dw"]), _ptr(o["dbias"]),
-                                     _ptr(o["dconv_state_in"]), _ptr(workspace), ws, _stream(stream)), "ssd_conv1d_bwd")
+        _check(_lib().ssd_conv1d_bwd(ctypes.byref(d), _at(xbc), xs, _at(w), _at(bias), _at(conv_state_in), _at(dout),
+                                     _at(dconv_state_out), _at(o["dxbc"]), _at(o["dw"]), _at(o["dbias"]),
+                                     _at(o["dconv_state_in"]), _at(workspace), ws, _stream(stream)), "ssd_conv1d_bwd")
     return o
 
 
@@ -1290,9 +1325,9 @@ def ssd_pool_copy(dst_pool, dst_idx, src_pool, src_idx, stacked=False, stream=No
     _need(dst_idx, "dst_idx", dev)
     _need(src_idx, "src_idx", dev)
     n = dst_idx.numel()
-    with _On(dev, stream):
-        _check(_lib().ssd_pool_copy(_ptr(dst_pool), dn, dls, _ptr(src_pool), sn, sls, slot, layers,
-                                    _ptr(_table(dst_idx, n, "dst_idx")), _ptr(_table(src_idx, n, "src_idx")), n,
+    with _on(dev, stream):
+        _check(_lib().ssd_pool_copy(_at(dst_pool), dn, dls, _at(src_pool), sn, sls, slot, layers,
+                                    _at(_table(dst_idx, n, "dst_idx")), _at(_table(src_idx, n, "src_idx")), n,
                                     _stream(stream)), "ssd_pool_copy")
     return dst_pool
 
@@ -1304,8 +1339,8 @@ def ssd_pool_clear(pool, slot_idx, stacked=False, stream=None):
     nslots, slot, layers, ls = _pool(pool, "pool", dev, stacked)
     _need(slot_idx, "slot_idx", dev)
     n = slot_idx.numel()
-    with _On(dev, stream):
-        _check(_lib().ssd_pool_clear(_ptr(pool), nslots, ls, slot, layers, _ptr(_table(slot_idx, n, "slot_idx")), n,
+    with _on(dev, stream):
+        _check(_lib().ssd_pool_clear(_at(pool), nslots, ls, slot, layers, _at(_table(slot_idx, n, "slot_idx")), n,
                                      _stream(stream)), "ssd_pool_clear")
     return pool
 
@@ -1319,12 +1354,13 @@ def ssd_pool_compact(slot_idx, nslots, stream=None):
     _need(slot_idx, "slot_idx", dev)
     n = slot_idx.numel()
     _table(slot_idx, n, "slot_idx")
-    with _On(dev, stream):
+    with _on(dev, stream):
         out = torch.empty((3, n), dtype=torch.int32, device=dev)
         count = torch.empty((), dtype=torch.int32, device=dev)
-        _check(_lib().ssd_pool_compact(_ptr(slot_idx), n, int(nslots), _ptr(out[0]), _ptr(out[1]), _ptr(out[2]),
-                                       _ptr(count), _stream(stream)), "ssd_pool_compact")
-    return out[0], out[1], out[2], count
+        src, dst, new = out.unbind(0)
+        _check(_lib().ssd_pool_compact(_at(slot_idx), n, int(nslots), _at(src), _at(dst), _at(new), _at(count),
+                                       _stream(stream)), "ssd_pool_compact")
+    return src, dst, new, count
 
 
 def split_xbc(v, nheads, head_dim, ngroups, d_state):

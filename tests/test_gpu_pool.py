@@ -85,9 +85,9 @@ def test_clear(slot):
 
 
 def host_plan(slots, nslots):
-    live = sorted({s for s in slots if 0 <= s < nslots})
-    count = len(live)
-    holes = [s for s in range(count) if s not in set(live)]
+    used = {s for s in slots if 0 <= s < nslots}
+    live, count = sorted(used), len(used)
+    holes = [s for s in range(count) if s not in used]
     movers = [s for s in live if s >= count]
     to = dict(zip(movers, holes))
     pad = [-1] * (len(slots) - len(movers))
