@@ -99,4 +99,27 @@ __device__ __forceinline__ SelBlock sel_block(int64_t id, int D, int G) {
     return r;
 }
 
+// v <- exp2(sum_k A2) v + end_k over `count` chunks k, `step` apart from `first` on (step may be negative):
+// sums + k ss and ends + k es + s D hold a chunk's sum of dt and its S states.  Four chunks are loaded
+// at a time: one after the other, their latencies would be most of a short chunk's time.
+template <int S>
+__device__ __forceinline__ void join_chunks(float (&v)[S], const float (&A2)[S], const float* sums, const float* ends, int first,
+                                            int count, int step, int64_t ss, int64_t es, int64_t D) {
+    for (int k = 0; k < count; k += 4) {
+        float sum[4], end[4][S];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t c = first + step * (k + i < count ? k + i : count - 1);
+            sum[i] = sums[c * ss];
+#pragma unroll
+            for (int s = 0; s < S; ++s) end[i][s] = ends[c * es + s * D];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (k + i < count)
+#pragma unroll
+                for (int s = 0; s < S; ++s) v[s] = fmaf(__builtin_amdgcn_exp2f(sum[i] * A2[s]), v[s], end[i][s]);
+    }
+}
+
 }  // namespace ssd

@@ -69,12 +69,7 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
         h[s] = Y && a.init_state ? a.init_state[so + s] : 0.f;
     }
     if constexpr (Y)
-        for (int p = 0; p < chunk; ++p) {
-            const float sum = ch.sums[(k.b * ch.n + p) * D + cs];
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                h[s] = fmaf(__builtin_amdgcn_exp2f(sum * A2[s]), h[s], ch.ends[((k.b * ch.n + p) * N + w * S + s) * D + cs]);
-        }
+        join_chunks(h, A2, ch.sums + k.b * ch.n * D + cs, ch.ends + (k.b * ch.n * N + w * S) * D + cs, 0, chunk, 1, D, N * D, D);
     T xr[TPT], zr[TPT], dr[TPT];     // the next tile's values as loaded
     float xk[TPT], zk[TPT], sum = 0.f;
     uint32_t ahead = 0;

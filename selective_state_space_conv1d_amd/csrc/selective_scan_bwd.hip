@@ -324,22 +324,13 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
             if constexpr (SPLIT) hin[j][s] = a.init_state ? a.init_state[so + s] : 0.f;
         }
         if constexpr (SPLIT) {
-            for (int p = 0; p < chunk; ++p) {
-                const float sum = ws[lay.csum + (b * lay.chunks + p) * D + c[j]];
+            const float *sums = ws + lay.csum + b * lay.chunks * D + c[j], *ends = ws + lay.ends + (b * lay.chunks * N + w * S) * D + c[j];
+            const float* grads = ws + lay.grads + (b * lay.chunks * N + w * S) * D + c[j];
+            join_chunks(hin[j], A2[j], sums, ends, 0, chunk, 1, D, N * D, D);
+            join_chunks(carry[j], A2[j], sums, grads, lay.chunks - 1, lay.chunks - 1 - chunk, -1, D, N * D, D);
 #pragma unroll
-                for (int s = 0; s < S; ++s)
-                    hin[j][s] = fmaf(__builtin_amdgcn_exp2f(sum * A2[j][s]), hin[j][s],
-                                     ws[lay.ends + ((b * lay.chunks + p) * N + w * S + s) * D + c[j]]);
-            }
-            for (int p = lay.chunks - 1; p > chunk; --p) {
-                const float sum = ws[lay.csum + (b * lay.chunks + p) * D + c[j]];
-#pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    carry[j][s] = fmaf(__builtin_amdgcn_exp2f(sum * A2[j][s]), carry[j][s],
-                                       ws[lay.grads + ((b * lay.chunks + p) * N + w * S + s) * D + c[j]]);
-                    if (!ok[j]) carry[j][s] = 0.f;
-                }
-            }
+            for (int s = 0; s < S; ++s)
+                if (!ok[j]) carry[j][s] = 0.f;
         }
     }
     T_ xr[TPT][P], dr[TPT][P], zr[TPT][P];   // the next tile's values as loaded
