@@ -78,9 +78,9 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
             const uint32_t t = static_cast<uint32_t>(first + w + W * i < last ? first + w + W * i : last);
-            xr[i] = *reinterpret_cast<const T*>(xp + static_cast<uint64_t>(t * xs) + le);
-            dr[i] = *reinterpret_cast<const T*>(dp + static_cast<uint64_t>(t * ds) + le);
-            if constexpr (GATE) zr[i] = *reinterpret_cast<const T*>(zp + static_cast<uint64_t>(t * zs) + le);
+            xr[i] = *reinterpret_cast<const T*>(xp + (le + t * xs));
+            dr[i] = *reinterpret_cast<const T*>(dp + (le + t * ds));
+            if constexpr (GATE) zr[i] = *reinterpret_cast<const T*>(zp + (le + t * zs));
         }
         // B and C of the tile, a token a lane: brings the rows, which each wave reads through the scalar
         // cache a few tokens before it needs them, near in time
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
             }
             char* base = yp - static_cast<int64_t>(kSelTile) * ys;
             auto store = [&](int i) {
-                *reinterpret_cast<TY*>(base + static_cast<uint64_t>(static_cast<uint32_t>(w + W * i) * ys) + lane * sizeof(TY)) = static_cast<TY>(y[i]);
+                *reinterpret_cast<TY*>(base + (static_cast<uint32_t>(lane * sizeof(TY)) + static_cast<uint32_t>(w + W * i) * ys)) = static_cast<TY>(y[i]);
             };
             if (ok && last >= kSelTile - 1) {
 #pragma unroll

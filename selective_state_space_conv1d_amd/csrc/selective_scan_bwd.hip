@@ -159,10 +159,10 @@ __global__ __launch_bounds__(64 * W) void selective_states_kernel(SelBwdArgs a, 
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
             const uint32_t t = static_cast<uint32_t>(first + w + W * i < last ? first + w + W * i : last);
-            xr[i] = *reinterpret_cast<const T_*>(xp + static_cast<uint64_t>(t * xs) + le);
-            dr[i] = *reinterpret_cast<const T_*>(dp + static_cast<uint64_t>(t * ds) + le);
-            if constexpr (SPLIT) gv[i] = *reinterpret_cast<const TY*>(gp + static_cast<uint64_t>(t * gs) + ge);
-            if constexpr (SPLIT && GATE) zr[i] = *reinterpret_cast<const T_*>(zp + static_cast<uint64_t>(t * zs) + le);
+            xr[i] = *reinterpret_cast<const T_*>(xp + (le + t * xs));
+            dr[i] = *reinterpret_cast<const T_*>(dp + (le + t * ds));
+            if constexpr (SPLIT) gv[i] = *reinterpret_cast<const TY*>(gp + (ge + t * gs));
+            if constexpr (SPLIT && GATE) zr[i] = *reinterpret_cast<const T_*>(zp + (le + t * zs));
         }
         const uint32_t t = static_cast<uint32_t>(first + (lane & 15) < last ? first + (lane & 15) : last);
         ahead = *reinterpret_cast<const uint32_t*>((SPLIT && (lane & 16) ? Cp : Bp) + static_cast<uint64_t>(t * bs));
@@ -351,10 +351,10 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const uint32_t o = static_cast<uint32_t>(c[j]) * E;
-                xr[i][j] = *reinterpret_cast<const T_*>(xp + static_cast<uint64_t>(t * xs) + o);
-                dr[i][j] = *reinterpret_cast<const T_*>(dp + static_cast<uint64_t>(t * ds) + o);
-                gv[i][j] = *reinterpret_cast<const TY*>(gp + static_cast<uint64_t>(t * gs) + static_cast<uint32_t>(c[j]) * static_cast<uint32_t>(sizeof(TY)));
-                if constexpr (GATE) zr[i][j] = *reinterpret_cast<const T_*>(zp + static_cast<uint64_t>(t * zs) + o);
+                xr[i][j] = *reinterpret_cast<const T_*>(xp + (o + t * xs));
+                dr[i][j] = *reinterpret_cast<const T_*>(dp + (o + t * ds));
+                gv[i][j] = *reinterpret_cast<const TY*>(gp + (static_cast<uint32_t>(c[j]) * static_cast<uint32_t>(sizeof(TY)) + t * gs));
+                if constexpr (GATE) zr[i][j] = *reinterpret_cast<const T_*>(zp + (o + t * zs));
             }
         }
     };
@@ -576,10 +576,10 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
             for (int j = 0; j < P; ++j) {
                 const uint32_t o = static_cast<uint32_t>(c[j]) * E;
                 auto store = [&](int i) {
-                    const uint64_t t = static_cast<uint32_t>(w + W * i) * ds;
-                    *reinterpret_cast<T_*>(dxp + t + o) = static_cast<T_>(dx[i][j]);
-                    *reinterpret_cast<T_*>(ddp + t + o) = static_cast<T_>(dd[i][j]);
-                    if constexpr (GATE) *reinterpret_cast<T_*>(dzp + t + o) = static_cast<T_>(y[i][j]);
+                    const uint32_t at = o + static_cast<uint32_t>(w + W * i) * ds;
+                    *reinterpret_cast<T_*>(dxp + at) = static_cast<T_>(dx[i][j]);
+                    *reinterpret_cast<T_*>(ddp + at) = static_cast<T_>(dd[i][j]);
+                    if constexpr (GATE) *reinterpret_cast<T_*>(dzp + at) = static_cast<T_>(y[i][j]);
                 };
                 if (!ragged && last >= T - 1) {
 #pragma unroll
