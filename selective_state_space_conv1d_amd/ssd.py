@@ -153,8 +153,16 @@ def _ptr(t):
     return None if t is None else _VP(t.data_ptr())
 
 
+# the current stream's handle and the current device without the objects around them (several times
+# cheaper than torch.cuda.current_stream and current_device, on the way of every call)
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_RAW_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream(stream):
     if stream is None:
+        if _RAW_STREAM is not None:
+            return _VP(_RAW_STREAM(_RAW_DEVICE()))
         stream = torch.cuda.current_stream()
     return _VP(stream.cuda_stream)
 
@@ -1091,7 +1099,7 @@ def _on(dev, stream):
     """Makes the tensors' device, and a given stream, current for the allocations and launches of one call.
     The buffers that the call allocates then belong to the stream that uses them."""
     if stream is None:
-        if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+        if dev.type != "cuda" or dev.index == _RAW_DEVICE():
             return _NOTHING
         return torch.cuda.device(dev)
     if stream.device != dev:
@@ -1104,10 +1112,14 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _like(t, dev, shape, dtype):
+    """Whether t is a tensor of this device, shape (a tuple) and dtype."""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+
+
 def _dense(t, name, dev, shape, dtype):
     """_need for a contiguous tensor, with a short way for one that is as it should be."""
-    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == dev
-            and t.is_contiguous()):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
         return t
     return _need(t, name, dev, shape, dtype)
 
@@ -1123,39 +1135,23 @@ def _workspace(size, workspace, dev):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _new(t, name, dev, shape, dtype):
-    """The caller's output t, checked, or a new tensor."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    return _dense(t, name, dev, shape, dtype)
-
-
-def _rows_of(t, name, dev, shape, dtype, lead, inner):
-    """The stride in elements between the token rows of t [*lead, ...], whose last axes (`inner` elements
-    together) must be packed and whose batch rows must be whole sequences apart."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == dev):
-        _need(t, name, dev, shape, dtype, contiguous=False)
-    Bt, L = lead if len(lead) == 2 else (1, lead[0])
-    if Bt * L == 0 or inner == 0:
+def _row_stride(st, name, lead, packed, inner):
+    """The stride in elements between the token rows of a tensor of strides st (leading axes `lead`, [B, L]
+    or [B]), whose batch rows must be whole sequences apart; packed: its last axes (`inner` elements) are."""
+    if 0 in lead:
         return inner
-    st = t.stride()
-    size = 1
-    for n, s in zip(reversed(shape[len(lead):]), reversed(st)):
-        if n > 1 and s != size:
-            raise ValueError(f"{name} must have packed {'channels' if len(shape) == len(lead) + 1 else '(G, N)'}")
-        size *= n
-    if len(lead) == 1:
-        return st[0] if L > 1 else inner
-    if L == 1:
-        return st[0] if Bt > 1 else inner
-    if Bt > 1 and st[0] != L * st[1]:
+    if not packed:
+        raise ValueError(f"{name} must have packed {'channels' if len(st) == len(lead) + 1 else '(G, N)'}")
+    if len(lead) == 1 or lead[1] == 1:
+        return st[0] if lead[0] > 1 else inner
+    if lead[0] > 1 and st[0] != lead[1] * st[1]:
         raise ValueError(f"{name} must have a uniform token stride")
     return st[1]
 
 
 def _selective_args(x, dt, A, B, C, D, z, dt_bias, rows):
     """Checks the inputs that every per-channel call has, x with `rows` leading axes (2: [B, L, D],
-    1: [B, D]); returns (device, D, G, N, strides of x, of B and C, of z)."""
+    1: [B, D]); returns (device, leading axes, D, G, N, strides of x, of B and C, of z)."""
     dev = _device(x, "x")
     shape, dtype = tuple(x.shape), x.dtype
     if len(shape) != rows + 1:
@@ -1163,24 +1159,44 @@ def _selective_args(x, dt, A, B, C, D, z, dt_bias, rows):
     lead, Dc = shape[:-1], shape[-1]
     if dtype not in _DT:
         raise ValueError(f"activations must be float32 or bfloat16 (got {dtype})")
-    _need(A, "A", dev, dtype=torch.float32)
-    if A.dim() != 2 or A.shape[0] != Dc:
-        raise ValueError(f"A must be [{Dc}, N]")
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError(f"A must be a tensor of shape [{Dc}, N]")
     N = A.shape[1]
+    _dense(A, "A", dev, (Dc, N), torch.float32)
     if not isinstance(B, torch.Tensor) or B.dim() != rows + 2:
         raise ValueError(f"B must be a tensor of {rows + 2} axes")
     G = B.shape[-2]
     if G == 0 or Dc % G:
         raise ValueError(f"the channels ({Dc}) must be a multiple of B's groups ({G})")
-    xs = _rows_of(x, "x", dev, shape, dtype, lead, Dc)
-    zs = Dc if z is None else _rows_of(z, "z", dev, shape, dtype, lead, Dc)
-    bcs = _rows_of(B, "B", dev, lead + (G, N), dtype, lead, G * N)
-    if _rows_of(C, "C", dev, lead + (G, N), dtype, lead, G * N) != bcs:
-        raise ValueError("B and C must share a token stride")
+    st = x.stride()
+    xs = _row_stride(st, "x", lead, st[-1] == 1 or Dc == 1, Dc)
+    zs = Dc
+    if z is not None:
+        _like(z, dev, shape, dtype) or _need(z, "z", dev, shape, dtype, contiguous=False)
+        st = z.stride()
+        zs = _row_stride(st, "z", lead, st[-1] == 1 or Dc == 1, Dc)
+    bshape = lead + (G, N)
+    _like(B, dev, bshape, dtype) or _need(B, "B", dev, bshape, dtype, contiguous=False)
+    _like(C, dev, bshape, dtype) or _need(C, "C", dev, bshape, dtype, contiguous=False)
+    st = B.stride()
+    bcs = _row_stride(st, "B", lead, (st[-1] == 1 or N == 1) and (G == 1 or st[-2] == N), G * N)
+    if C.stride() != st:
+        st = C.stride()
+        if _row_stride(st, "C", lead, (st[-1] == 1 or N == 1) and (G == 1 or st[-2] == N), G * N) != bcs:
+            raise ValueError("B and C must share a token stride")
     _dense(dt, "dt", dev, shape, dtype)
     D is None or _dense(D, "D", dev, (Dc,), torch.float32)
     dt_bias is None or _dense(dt_bias, "dt_bias", dev, (Dc,), torch.float32)
-    return dev, Dc, G, N, xs, bcs, zs
+    return dev, lead, Dc, G, N, xs, bcs, zs
+
+
+def _new_y(y, dt, y_dtype, dev):
+    """The caller's y, checked, or a new one of dt's shape."""
+    if y is not None:
+        return _dense(y, "y", dev, tuple(dt.shape), y_dtype or y.dtype)
+    if y_dtype is None or y_dtype is dt.dtype:
+        return torch.empty_like(dt)
+    return torch.empty(dt.shape, dtype=y_dtype, device=dev)
 
 
 def ssd_selective_scan(x, dt, A, B, C, D=None, z=None, init_state=None, final_state=None, y=None, y_dtype=None,
@@ -1190,14 +1206,12 @@ def ssd_selective_scan(x, dt, A, B, C, D=None, z=None, init_state=None, final_st
     rows may be strided by a multiple of 16 bytes), skip weights D [D] fp32|None, init_state/final_state
     [B, D, N] fp32|None (may be the same tensor).  dt_bias, dt_softplus and dt_limit as ssd_chunk_scan.
     N 16, 32, 64 or 128.  Returns y [B, L, D] in y_dtype (default x's)."""
-    dev, Dc, G, N, xs, bcs, zs = _selective_args(x, dt, A, B, C, D, z, dt_bias, 2)
-    Bt, L = x.shape[:2]
+    dev, (Bt, L), Dc, G, N, xs, bcs, zs = _selective_args(x, dt, A, B, C, D, z, dt_bias, 2)
     init_state is None or _dense(init_state, "init_state", dev, (Bt, Dc, N), torch.float32)
     final_state is None or _dense(final_state, "final_state", dev, (Bt, Dc, N), torch.float32)
     with _on(dev, stream):
-        ydt = y_dtype or (x.dtype if y is None else y.dtype)
-        y = _new(y, "y", dev, (Bt, L, Dc), ydt)
-        d = _dims(Bt, L, Dc, 1, G, N, x.dtype, ydt)
+        y = _new_y(y, dt, y_dtype, dev)
+        d = _dims(Bt, L, Dc, 1, G, N, x.dtype, y.dtype)
         workspace, ws = _workspace(int(_lib().ssd_selective_scan_workspace_size(ctypes.byref(d))), workspace, dev)
         _check(_lib().ssd_selective_scan(ctypes.byref(d), _at(x), xs, _at(dt), _at(A), _at(B), _at(C), bcs, _at(D),
                                          _at(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit), _at(init_state),
@@ -1212,8 +1226,7 @@ def ssd_selective_scan_bwd(dy, x, dt, A, B, C, D=None, z=None, init_state=None, 
     dfinal_state [B, D, N] fp32|None.  Returns a dict: dx, ddt, dz [B, L, D] and dB, dC [B, L, G, N] in x's
     dtype, dA [D, N], dD [D], ddt_bias [D] and dinit_state [B, D, N] in fp32; None where the input is
     None."""
-    dev, Dc, G, N, xs, bcs, zs = _selective_args(x, dt, A, B, C, D, z, dt_bias, 2)
-    Bt, L = x.shape[:2]
+    dev, (Bt, L), Dc, G, N, xs, bcs, zs = _selective_args(x, dt, A, B, C, D, z, dt_bias, 2)
     _need(dy, "dy", dev, (Bt, L, Dc))
     init_state is None or _dense(init_state, "init_state", dev, (Bt, Dc, N), torch.float32)
     dfinal_state is None or _dense(dfinal_state, "dfinal_state", dev, (Bt, Dc, N), torch.float32)
@@ -1242,21 +1255,20 @@ def ssd_selective_state_update(state, x, dt, A, B, C, D=None, z=None, slot_idx=N
     [nslots, D, N]; updated in place, or with state_out (same shape, other memory) read there and written
     here, the named entries alone.  x, z [B, D] and B/C [B, G, N] (rows may be strided), dt [B, D].
     Returns y [B, D]."""
-    dev, Dc, G, N, xs, bcs, zs = _selective_args(x, dt, A, B, C, D, z, dt_bias, 1)
-    Bt = x.shape[0]
-    _need(state, "state", dev, dtype=torch.float32)
-    if state.dim() != 3 or tuple(state.shape[1:]) != (Dc, N):
+    dev, (Bt,), Dc, G, N, xs, bcs, zs = _selective_args(x, dt, A, B, C, D, z, dt_bias, 1)
+    if not isinstance(state, torch.Tensor) or state.dim() != 3:
         raise ValueError(f"state must be [B or nslots, {Dc}, {N}]")
-    state_out is None or _dense(state_out, "state_out", dev, tuple(state.shape), torch.float32)
+    sshape = (state.shape[0], Dc, N)
+    _dense(state, "state", dev, sshape, torch.float32)
+    state_out is None or _dense(state_out, "state_out", dev, sshape, torch.float32)
     _need(slot_idx, "slot_idx", dev, optional=True)
     if state_out is not None and state_out.data_ptr() != state.data_ptr() and state.numel() > 0 and \
             abs(state_out.data_ptr() - state.data_ptr()) < 4 * state.numel():
         raise ValueError("state_out must be state or not overlap it")
     st, nslots, tab = _state_pool_args(state, slot_idx, Bt)
     with _on(dev, stream):
-        ydt = y_dtype or (x.dtype if y is None else y.dtype)
-        y = _new(y, "y", dev, (Bt, Dc), ydt)
-        d = _dims(Bt, 1, Dc, 1, G, N, x.dtype, ydt)
+        y = _new_y(y, dt, y_dtype, dev)
+        d = _dims(Bt, 1, Dc, 1, G, N, x.dtype, y.dtype)
         _check(_lib().ssd_selective_state_update(ctypes.byref(d), _at(st), _at(st if state_out is None else state_out),
                                                  _at(tab), nslots, _at(x), xs, _at(dt), _at(A), _at(B), _at(C), bcs,
                                                  _at(D), _at(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
@@ -1297,17 +1309,26 @@ def ssd_conv1d_bwd(dout, xbc, w, bias=None, conv_state_in=None, dconv_state_out=
 
 # --------------------------------------------------------------------------- slots of state pools
 def _pool(pool, name, dev, stacked):
-    """(slots, bytes of a slot, layers, layer stride) of pool [nslots, ...], or [layers, nslots, ...]."""
-    _need(pool, name, dev)
-    lead = 2 if stacked else 1
-    if pool.dim() < lead:
+    """(layers, slots, a slot's shape, its bytes) of pool [nslots, ...], or [layers, nslots, ...]."""
+    if not (isinstance(pool, torch.Tensor) and pool.device == dev and pool.is_contiguous()):
+        _need(pool, name, dev)
+    shape = tuple(pool.shape)
+    if len(shape) < (2 if stacked else 1):
         raise ValueError(f"{name} must be [{'layers, ' if stacked else ''}nslots, ...]")
-    layers = pool.shape[0] if stacked else 1
-    nslots = pool.shape[lead - 1]
-    slot = pool.element_size()
-    for n in pool.shape[lead:]:
-        slot *= n
-    return nslots, slot, layers, nslots * slot
+    layers, nslots, slot = (shape[0], shape[1], shape[2:]) if stacked else (1, shape[0], shape[1:])
+    size = pool.element_size()
+    for n in slot:
+        size *= n
+    return layers, nslots, slot, size
+
+
+def _slots(t, n, name, dev):
+    """An int32 table of n slots (of any length with n None) on the device."""
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.dim() == 1 and (n is None or t.shape[0] == n)
+            and t.device == dev and t.is_contiguous()):
+        return t
+    _need(t, name, dev)
+    return _table(t, t.numel() if n is None else n, name)
 
 
 def ssd_pool_copy(dst_pool, dst_idx, src_pool, src_idx, stacked=False, stream=None):
@@ -1317,18 +1338,18 @@ def ssd_pool_copy(dst_pool, dst_idx, src_pool, src_idx, stacked=False, stream=No
     layer is copied alike); the two may be one tensor.  dst_idx, src_idx [n] int32; an entry with an
     index that names no slot is skipped."""
     dev = _device(dst_pool, "dst_pool")
-    dn, slot, layers, dls = _pool(dst_pool, "dst_pool", dev, stacked)
-    sn, sslot, slayers, sls = _pool(src_pool, "src_pool", dev, stacked)
-    lead = 2 if stacked else 1
-    if dst_pool.dtype != src_pool.dtype or dst_pool.shape[lead:] != src_pool.shape[lead:] or layers != slayers:
-        raise ValueError("both pools must have the same dtype, slot shape and layers")
-    _need(dst_idx, "dst_idx", dev)
-    _need(src_idx, "src_idx", dev)
-    n = dst_idx.numel()
+    layers, dn, slot, size = _pool(dst_pool, "dst_pool", dev, stacked)
+    sn = dn
+    if src_pool is not dst_pool:
+        slayers, sn, sslot, _ = _pool(src_pool, "src_pool", dev, stacked)
+        if dst_pool.dtype != src_pool.dtype or slot != sslot or layers != slayers:
+            raise ValueError("both pools must have the same dtype, slot shape and layers")
+    _slots(dst_idx, None, "dst_idx", dev)
+    n = dst_idx.shape[0]
+    _slots(src_idx, n, "src_idx", dev)
     with _on(dev, stream):
-        _check(_lib().ssd_pool_copy(_at(dst_pool), dn, dls, _at(src_pool), sn, sls, slot, layers,
-                                    _at(_table(dst_idx, n, "dst_idx")), _at(_table(src_idx, n, "src_idx")), n,
-                                    _stream(stream)), "ssd_pool_copy")
+        _check(_lib().ssd_pool_copy(_at(dst_pool), dn, dn * size, _at(src_pool), sn, sn * size, size, layers,
+                                    _at(dst_idx), _at(src_idx), n, _stream(stream)), "ssd_pool_copy")
     return dst_pool
 
 
@@ -1336,12 +1357,11 @@ def ssd_pool_clear(pool, slot_idx, stacked=False, stream=None):
     """Zeroes the slots slot_idx [n] int32 of pool [nslots, ...] (or of every layer of [layers, nslots, ...]
     with stacked), in place; indices that name no slot are skipped."""
     dev = _device(pool, "pool")
-    nslots, slot, layers, ls = _pool(pool, "pool", dev, stacked)
-    _need(slot_idx, "slot_idx", dev)
-    n = slot_idx.numel()
+    layers, nslots, _, size = _pool(pool, "pool", dev, stacked)
+    n = _slots(slot_idx, None, "slot_idx", dev).shape[0]
     with _on(dev, stream):
-        _check(_lib().ssd_pool_clear(_at(pool), nslots, ls, slot, layers, _at(_table(slot_idx, n, "slot_idx")), n,
-                                     _stream(stream)), "ssd_pool_clear")
+        _check(_lib().ssd_pool_clear(_at(pool), nslots, nslots * size, size, layers, _at(slot_idx), n, _stream(stream)),
+               "ssd_pool_clear")
     return pool
 
 
@@ -1351,9 +1371,7 @@ def ssd_pool_compact(slot_idx, nslots, stream=None):
     device: ssd_pool_copy(pool, dst_idx, pool, src_idx) makes the moves in each pool that the table serves,
     new_slot_idx replaces the table, and slots from count on are free."""
     dev = _device(slot_idx, "slot_idx")
-    _need(slot_idx, "slot_idx", dev)
-    n = slot_idx.numel()
-    _table(slot_idx, n, "slot_idx")
+    n = _slots(slot_idx, None, "slot_idx", dev).shape[0]
     with _on(dev, stream):
         out = torch.empty((3, n), dtype=torch.int32, device=dev)
         count = torch.empty((), dtype=torch.int32, device=dev)

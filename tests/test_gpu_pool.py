@@ -70,6 +70,18 @@ def test_copy_of_many_entries():
     assert torch.equal(got.cpu(), want)
 
 
+def test_pools_past_32_bits():
+    pool = torch.zeros(2, 9, 300 << 20, dtype=torch.int8, device=DEV)      # slots of 300 MiB: layer 1 lies past 2 GiB
+    pool[1, 8, ::4097] = torch.arange(pool[1, 8, ::4097].numel(), device=DEV).to(torch.int8)
+    pool[0, 8, -5:] = 7
+    ssd.ssd_pool_copy(pool, i32([0, 7]), pool, i32([8, 8]), stacked=True)
+    for d in (0, 7):
+        assert torch.equal(pool[0, d], pool[0, 8]) and torch.equal(pool[1, d], pool[1, 8])
+    assert int(pool[:, 1:7].count_nonzero()) == 0
+    ssd.ssd_pool_clear(pool, i32([8]), stacked=True)
+    assert int(pool[:, 8].count_nonzero()) == 0
+
+
 def test_infinities_and_nans_are_bytes():
     pool = torch.tensor([[float("nan"), float("inf"), -0.0, 1.0], [0.0, 0, 0, 0]])
     got = pool.to(DEV)

@@ -39,7 +39,9 @@ def k_of(L, N):
 ARGS = ("x", "dt", "A", "B", "C", "D", "z")
 # batch, tokens, channels, groups, states: one token; a tile's border; channels that end inside a
 # workgroup, groups that do; every state count; several tiles; more than one batch entry
-SIZES = [(1, 1, 8, 1, 16), (2, 16, 64, 1, 16), (1, 17, 72, 1, 16), (2, 37, 200, 2, 16), (3, 100, 40, 1, 32),
+# (sequences of 128 tokens and more are cut into chunks at these sizes, the last one is not)
+SIZES = [(1, 140, 72, 1, 32), (1, 130, 40, 2, 64), (2, 133, 66, 1, 128), (512, 130, 8, 1, 16),
+         (1, 1, 8, 1, 16), (2, 16, 64, 1, 16), (1, 17, 72, 1, 16), (2, 37, 200, 2, 16), (3, 100, 40, 1, 32),
          (1, 65, 96, 2, 64), (2, 33, 130, 1, 128), (1, 300, 64, 1, 16), (1, 5, 1, 1, 32), (1, 15, 66, 3, 64)]
 
 
@@ -80,6 +82,28 @@ def test_gradient(size, dtype, ydt):
         assert (got[name] is None) == (r[name] is None), name
         if r[name] is not None:
             ref.check(got[name], r[name], m[name], k, name)
+
+
+def test_offsets_past_32_bits():
+    """Token rows 2^23 elements apart: the last ones lie past 4 GiB, on their own and in the whole call."""
+    L, D, N, rs = 300, 72, 16, 1 << 23
+    s = make(1, L, D, 1, N, BF, 23)
+    wide = {k: torch.empty((L, rs), dtype=BF, device=DEV) for k in ("x", "z")}
+    t = dict(s)
+    for k, v in wide.items():
+        v[:, 8:8 + D] = s[k][0]
+        t[k] = v[None, :, 8:8 + D]
+    y, final = forward(t)
+    yc, finalc = forward(s)
+    assert torch.equal(y, yc) and torch.equal(final, finalc)
+    a, b = (ssd.ssd_selective_scan_bwd(q["dy"], *[q[k] for k in ARGS], init_state=q["init"], dt_bias=q["dt_bias"], dt_softplus=True) for q in (t, s))
+    assert all(v is None or torch.equal(v, b[k]) for k, v in a.items())
+    w = torch.rand(128, 4, device=DEV).to(BF)
+    x = wide["x"][None, :, :128]
+    wide["x"][:, :128] = torch.randn(L, 128, device=DEV).to(BF)
+    dout = torch.randn(1, L, 128, device=DEV).to(BF)
+    a, b = ssd.ssd_conv1d_bwd(dout, x, w), ssd.ssd_conv1d_bwd(dout, x.contiguous(), w)
+    assert all(v is None or torch.equal(v, b[k]) for k, v in a.items())
 
 
 @pytest.mark.parametrize("softplus,limit,bias", [(False, None, False), (True, (0.05, 0.4), True), (False, (-0.2, 0.3), True)])
