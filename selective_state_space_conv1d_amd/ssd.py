@@ -1227,18 +1227,16 @@ def ssd_selective_scan_bwd(dy, x, dt, A, B, C, D=None, z=None, init_state=None, 
     dtype, dA [D, N], dD [D], ddt_bias [D] and dinit_state [B, D, N] in fp32; None where the input is
     None."""
     dev, (Bt, L), Dc, G, N, xs, bcs, zs = _selective_args(x, dt, A, B, C, D, z, dt_bias, 2)
-    _need(dy, "dy", dev, (Bt, L, Dc))
+    _dense(dy, "dy", dev, (Bt, L, Dc), x.dtype) if getattr(dy, "dtype", None) is x.dtype else _need(dy, "dy", dev, (Bt, L, Dc))
     init_state is None or _dense(init_state, "init_state", dev, (Bt, Dc, N), torch.float32)
     dfinal_state is None or _dense(dfinal_state, "dfinal_state", dev, (Bt, Dc, N), torch.float32)
     d = _dims(Bt, L, Dc, 1, G, N, x.dtype, dy.dtype)
     with _on(dev, stream):
-        def new(like, shape, dtype):
-            return None if like is None else torch.empty(shape, dtype=dtype, device=dev)
-
-        o = {"dx": new(x, x.shape, x.dtype), "ddt": new(x, x.shape, x.dtype), "dA": new(A, A.shape, A.dtype),
-             "dB": new(B, B.shape, x.dtype), "dC": new(C, C.shape, x.dtype), "dD": new(D, (Dc,), torch.float32),
-             "dz": new(z, x.shape, x.dtype), "ddt_bias": new(dt_bias, (Dc,), torch.float32),
-             "dinit_state": new(init_state, (Bt, Dc, N), torch.float32)}
+        new = torch.empty_like                 # of contiguous tensors
+        o = {"dx": new(dt), "ddt": new(dt), "dA": new(A), "dB": torch.empty((Bt, L, G, N), dtype=x.dtype, device=dev),
+             "dC": torch.empty((Bt, L, G, N), dtype=x.dtype, device=dev), "dD": None if D is None else new(D),
+             "dz": None if z is None else new(dt), "ddt_bias": None if dt_bias is None else new(dt_bias),
+             "dinit_state": None if init_state is None else new(init_state)}
         workspace, ws = _workspace(int(_lib().ssd_selective_scan_bwd_workspace_size(ctypes.byref(d))), workspace, dev)
         _check(_lib().ssd_selective_scan_bwd(ctypes.byref(d), _at(dy), _at(x), xs, _at(dt), _at(A), _at(B), _at(C),
                                              bcs, _at(D), _at(z), zs, _dt_params(dt_bias, dt_softplus, dt_limit),
@@ -1288,18 +1286,17 @@ def ssd_conv1d_bwd(dout, xbc, w, bias=None, conv_state_in=None, dconv_state_out=
     if L > 0 and ((xbc.stride(2) != 1 and CD > 1) or (L > 1 and not _uniform_rows(xbc, L))):
         raise ValueError("xbc must be [B, L, CD] with packed channels and uniform token stride")
     H, P, G, N = _split_cd(CD, nheads, head_dim, ngroups, d_state)
-    _conv_params(dev, CD, xbc.dtype, w, bias)
+    _dense(w, "w", dev, (CD, 4), xbc.dtype)
+    bias is None or _dense(bias, "bias", dev, (CD,), xbc.dtype)
     _dense(dout, "dout", dev, (Bt, L, CD), xbc.dtype)
     conv_state_in is None or _dense(conv_state_in, "conv_state_in", dev, (Bt, CD, 4), xbc.dtype)
     dconv_state_out is None or _dense(dconv_state_out, "dconv_state_out", dev, (Bt, CD, 4), xbc.dtype)
     d = _dims(Bt, L, H, P, G, N, xbc.dtype, xbc.dtype)
     xs = CD if Bt * L <= 1 else xbc.stride(1) if L > 1 else xbc.stride(0)
     with _on(dev, stream):
-        def new(like, shape, dtype):
-            return None if like is None else torch.empty(shape, dtype=dtype, device=dev)
-
-        o = {"dxbc": new(xbc, (Bt, L, CD), xbc.dtype), "dw": new(w, (CD, 4), torch.float32),
-             "dbias": new(bias, (CD,), torch.float32), "dconv_state_in": new(conv_state_in, (Bt, CD, 4), xbc.dtype)}
+        o = {"dxbc": torch.empty_like(dout), "dw": torch.empty((CD, 4), dtype=torch.float32, device=dev),
+             "dbias": None if bias is None else torch.empty((CD,), dtype=torch.float32, device=dev),
+             "dconv_state_in": None if conv_state_in is None else torch.empty_like(conv_state_in)}
         workspace, ws = _workspace(int(_lib().ssd_conv1d_bwd_workspace_size(ctypes.byref(d))), workspace, dev)
         _check(_lib().ssd_conv1d_bwd(ctypes.byref(d), _at(xbc), xs, _at(w), _at(bias), _at(conv_state_in), _at(dout),
                                      _at(dconv_state_out), _at(o["dxbc"]), _at(o["dw"]), _at(o["dbias"]),
