@@ -6,8 +6,9 @@
 //   dz = dout y silu'(z), and through the dt prologue: ddt_raw = ddt sigmoid(dt_raw + bias) (0 where clamped)
 //
 // Three launches.  (1) states: the forward recurrence alone, which leaves the state at the start of
-// every tile of T tokens in the workspace.  (2) gradients: tiles from last to first; each tile's a and q
-// are recomputed into registers (64 of each) on the way forward and used on the way back.  (3) sums:
+// every tile of T tokens in the workspace.  (2) gradients: tiles from last to first; each tile's a and h
+// are recomputed into registers (64 of each) on the way forward and used on the way back, where
+// g_t q_t = (a_t g_t) h_{t-1} needs no q.  (3) sums:
 // partial sums to dA, dDskip, ddt_bias, dB and dC, in a fixed order, so results do not depend on
 // scheduling.  Long sequences are cut into chunks as in the forward: then (1) runs every chunk from a
 // zero state and also leaves what a chunk's own outputs make of the gradient at its start, and (2)
@@ -21,6 +22,8 @@
 // instruction against a one-hot operand takes fewer instructions, but holds the vector pipe for all of
 // its 32 cycles: 544 us for the gradients launch at 4 x 2048 x 4096 channels.)
 #include "selective_device.h"
+
+#include <type_traits>
 
 namespace ssd {
 
@@ -204,39 +207,45 @@ __global__ __launch_bounds__(64 * W) void selective_states_kernel(SelBwdArgs a, 
             d[0][t] = st[buf][t][lane];
             if constexpr (SPLIT) y[0][t] = sdy[buf][t][lane];
         }
+        // the first chunk's gradient at its start is nobody's
+        auto tile = [&](auto with_g) {
+            constexpr bool WITH_G = decltype(with_g)::value;
 #pragma unroll
-        for (int u = 0; u < kStatesTile; u += SUB) {
-            const int at = (u / SUB) & 1;
-            rows[at ^ 1].template load<SPLIT>(Bp, Cp, bs, u + SUB, last);
-            if (u + SUB < kStatesTile)
+            for (int u = 0; u < kStatesTile; u += SUB) {
+                const int at = (u / SUB) & 1;
+                rows[at ^ 1].template load<SPLIT>(Bp, Cp, bs, u + SUB, last);
+                if (u + SUB < kStatesTile)
+#pragma unroll
+                    for (int t = 0; t < SUB; ++t) {
+                        d[at ^ 1][t] = st[buf][u + SUB + t][lane];
+                        if constexpr (SPLIT) y[at ^ 1][t] = sdy[buf][u + SUB + t][lane];
+                    }
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int t = 0; t < SUB; ++t) {
-                    d[at ^ 1][t] = st[buf][u + SUB + t][lane];
-                    if constexpr (SPLIT) y[at ^ 1][t] = sdy[buf][u + SUB + t][lane];
-                }
-            __builtin_amdgcn_sched_barrier(0);
+                    if ((u + t) % T == 0 && u + t <= last) {
+                        // the state at the start of a tile, and the chunk's sum of dt before it
+                        if (ok) {
 #pragma unroll
-            for (int t = 0; t < SUB; ++t) {
-                if ((u + t) % T == 0 && u + t <= last) {
-                    // the state at the start of a tile, and the chunk's sum of dt before it
-                    if (ok) {
-#pragma unroll
-                        for (int s = 0; s < S; ++s) cp[static_cast<int64_t>((u + t) / T * N + s) * D] = h[s];
-                        if (SPLIT && w == 0) tp[static_cast<int64_t>((u + t) / T) * D] = dsum;
+                            for (int s = 0; s < S; ++s) cp[static_cast<int64_t>((u + t) / T * N + s) * D] = h[s];
+                            if (SPLIT && w == 0) tp[static_cast<int64_t>((u + t) / T) * D] = dsum;
+                        }
                     }
-                }
-                if constexpr (SPLIT) dsum += d[at][t].x;
+                    if constexpr (SPLIT) dsum += d[at][t].x;
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    const float e = __builtin_amdgcn_exp2f(d[at][t].x * A2[s]);
-                    h[s] = fmaf(e, h[s], d[at][t].y * rows[at].b(t, s));
-                    if constexpr (SPLIT) {
-                        p[s] *= e;
-                        gr[s] = fmaf(p[s], rows[at].c(t, s) * y[at][t], gr[s]);
+                    for (int s = 0; s < S; ++s) {
+                        const float e = __builtin_amdgcn_exp2f(d[at][t].x * A2[s]);
+                        h[s] = fmaf(e, h[s], d[at][t].y * rows[at].b(t, s));
+                        if constexpr (WITH_G) {
+                            p[s] *= e;
+                            gr[s] = fmaf(p[s], rows[at].c(t, s) * y[at][t], gr[s]);
+                        }
                     }
                 }
             }
-        }
+        };
+        if (SPLIT && chunk > 0) tile(std::integral_constant<bool, SPLIT>{});
+        else tile(std::false_type{});
         xp += static_cast<int64_t>(kStatesTile) * xs;
         dp += static_cast<int64_t>(kStatesTile) * ds;
         if constexpr (SPLIT) gp += static_cast<int64_t>(kStatesTile) * gs;
@@ -437,7 +446,11 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
 #pragma unroll
                 for (int s = 0; s < S; ++s) h[j][s] = fmaf(__builtin_amdgcn_exp2f(ts[j] * A2[j][s]), hin[j][s], h[j][s]);
         __syncthreads();
-        float q[T][P][S], ea[T][P][S];
+        float hs[T + 1][P][S], ea[T][P][S];   // states before each token and after the last; decays
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+#pragma unroll
+            for (int s = 0; s < S; ++s) hs[0][j][s] = h[j][s];
         float2 dn[2][P];
 #pragma unroll
         for (int j = 0; j < P; ++j) dn[0][j] = st[0][j][lane];
@@ -461,17 +474,13 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
                         ea[t][j][s] = __builtin_amdgcn_exp2f(d.x * A2[j][s]);
-                        q[t][j][s] = ea[t][j][s] * h[j][s];
-                        h[j][s] = fmaf(d.y, rows[at].b(v, s), q[t][j][s]);
-                        if constexpr (GATE) y = fmaf(h[j][s], rows[at].c(v, s), y);
+                        hs[t + 1][j][s] = fmaf(ea[t][j][s], hs[t][j][s], d.y * rows[at].b(v, s));
+                        if constexpr (GATE) y = fmaf(hs[t + 1][j][s], rows[at].c(v, s), y);
                     }
                     if constexpr (GATE) ypart[w][t][j][lane] = y;
                 }
             }
         }
-        // the next tile's loads; h is free from here on
-        load(tile > 0 ? tile - 1 : 0);
-        load_state(tile > 0 ? tile - 1 : 0);
         float yn[2][P];
 #pragma unroll
         for (int j = 0; j < P; ++j) yn[(T - 1) & 1][j] = sdy[T - 1][j][lane];
@@ -500,14 +509,13 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
                         const float g = fmaf(rows[at].c(v, s), dy, carry[j][s]);
-                        const float hv = fmaf(d.y, rows[at].b(v, s), q[t][j][s]);
                         pB[s] = j == 0 ? g * d.y : fmaf(g, d.y, pB[s]);
-                        pC[s] = j == 0 ? dy * hv : fmaf(dy, hv, pC[s]);
+                        pC[s] = j == 0 ? dy * hs[t + 1][j][s] : fmaf(dy, hs[t + 1][j][s], pC[s]);
                         gB = fmaf(g, rows[at].b(v, s), gB);
-                        const float x = g * q[t][j][s];
+                        carry[j][s] = ea[t][j][s] * g;
+                        const float x = carry[j][s] * hs[t][j][s];
                         dA[j][s] = fmaf(d.x, x, dA[j][s]);
                         gA = fmaf(A2[j][s], x, gA);
-                        carry[j][s] = ea[t][j][s] * g;
                     }
                     part[w][t][j][lane] = make_float2(gB, gA);
                 }
@@ -518,6 +526,10 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
                     vals[S + s] = pC[s];
                 }
                 tok[t] = merge_all<0>(vals, lane);
+                if (t == T - 1) {   // the next tile's loads, once the last token's state and decay are free
+                    load(tile > 0 ? tile - 1 : 0);
+                    load_state(tile > 0 ? tile - 1 : 0);
+                }
             }
         }
         // dA's products are added here and not, as the compiler would have it, after the next barrier
@@ -637,14 +649,17 @@ __global__ __launch_bounds__(256) void selective_sums_kernel(SelBwdArgs a, const
         else if (a.ddt_bias) a.ddt_bias[i - (N + 1) * D] = v;
         return;
     }
-    i -= (N + 2) * D;
+    i = 4 * (i - (N + 2) * D);   // four values a thread: N is a multiple of 4
     if (i >= rows * 2 * G * N) return;
     const int64_t n = i % N, which = i / N % 2, g = i / (2 * N) % G, row = i / (2 * N * G);
     const int64_t per = lay.blocks / G;
     const float* p = ws + lay.dBC + (g * per * rows + row) * 2 * N + which * N + n;
-    float v = 0.f;
-    for (int64_t k = 0; k < per; ++k) v += p[k * rows * 2 * N];
-    (which ? static_cast<T*>(a.dC) : static_cast<T*>(a.dB))[(row * G + g) * N + n] = static_cast<T>(v);
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int64_t k = 0; k < per; ++k) v += *reinterpret_cast<const f32x4*>(p + k * rows * 2 * N);
+    T* o = (which ? static_cast<T*>(a.dC) : static_cast<T*>(a.dB)) + (row * G + g) * N + n;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = static_cast<T>(v[k]);
 }
 
 template <typename T, typename TY, int N, bool SPLIT, bool GATE>
@@ -665,7 +680,7 @@ static hipError_t bwd_n(const SelBwdArgs& a, float* ws, hipStream_t s) {
         if (lay.chunks > 1) a.z ? bwd_main<T, TY, N, true, true>(a, ws, lay, s) : bwd_main<T, TY, N, true, false>(a, ws, lay, s);
         else a.z ? bwd_main<T, TY, N, false, true>(a, ws, lay, s) : bwd_main<T, TY, N, false, false>(a, ws, lay, s);
     }
-    const int64_t n = (a.d_state + 2) * static_cast<int64_t>(a.channels) + a.batch * a.seqlen * 2 * a.ngroups * a.d_state;
+    const int64_t n = (a.d_state + 2) * static_cast<int64_t>(a.channels) + a.batch * a.seqlen * a.ngroups * a.d_state / 2;
     hipLaunchKernelGGL((selective_sums_kernel<T>), dim3(static_cast<uint32_t>((n + 255) / 256)), dim3(256), 0, s, a, ws, lay);
     return hipGetLastError();
 }
