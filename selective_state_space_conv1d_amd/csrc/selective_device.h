@@ -8,6 +8,13 @@ namespace ssd {
 // Decay exponents are kept in base 2.
 constexpr float kLog2e = 1.44269504088896340736f;
 
+// A in base 2.  Minus infinity (a channel that forgets everything) becomes the lowest number: where a tile
+// ends after the last token dt is 0, and 0 times infinity would not be 0.
+__device__ __forceinline__ float base2_rate(float A) {
+    const float r = A * kLog2e;
+    return r == -__builtin_inff() ? -3.402823466e38f : r;
+}
+
 // dt of one (token, channel): + bias, softplus, clamp, as dt_prologue; softplus by the identity
 // log1p(e) = e log(u) / (u - 1), u = 1 + e, whose rounding errors cancel (about 3e-7 relative).
 struct SelDt {

@@ -19,8 +19,8 @@ namespace ssd {
 constexpr int kSelTile = 16;   // tokens staged at a time
 
 // Sequences are cut into chunks of `tokens` when there are too few workgroups otherwise (sel_chunks).
-// Then a first launch (Y false) runs each chunk but the last from a zero state and leaves its final
-// state [B][chunks][N][D] and its sum of dt [B][chunks][D]; a chunk's state at its first token follows from
+// Then a first launch (Y false) runs each chunk but the last, the first from the initial state and the
+// others from zero, and leaves its final state [B][chunks][N][D] and its sum of dt [B][chunks][D]; a chunk's state at its first token follows from
 // those of the chunks before it, since a chunk multiplies the state it starts from by exp(A sum dt).
 struct SelChunks {
     int64_t tokens;
@@ -65,11 +65,21 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
     const int64_t so = (k.b * D + cs) * N + w * S;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        A2[s] = a.A[static_cast<int64_t>(cs) * N + w * S + s] * kLog2e;
-        h[s] = Y && a.init_state ? a.init_state[so + s] : 0.f;
+        A2[s] = base2_rate(a.A[static_cast<int64_t>(cs) * N + w * S + s]);
+        h[s] = (ch.n == 1 || (!Y && chunk == 0)) && a.init_state ? a.init_state[so + s] : 0.f;
     }
-    if constexpr (Y)
-        join_chunks(h, A2, ch.sums + k.b * ch.n * D + cs, ch.ends + (k.b * ch.n * N + w * S) * D + cs, 0, chunk, 1, D, N * D, D);
+    // the first launch of a chunked scan keeps the initial state in the last chunk's place, which has no
+    // other use: in the second the final state may be written over it before all have read it
+    float* ends = ch.ends + (k.b * ch.n * N + w * S) * D + cs;
+    if (!Y && chunk == 0 && ok)
+#pragma unroll
+        for (int s = 0; s < S; ++s) ends[((ch.n - 1) * N + s) * D] = h[s];
+    if (Y && ch.n > 1) {
+        if (chunk == 0)
+#pragma unroll
+            for (int s = 0; s < S; ++s) h[s] = ends[((ch.n - 1) * N + s) * D];
+        join_chunks(h, A2, ch.sums + k.b * ch.n * D + cs, ends, 0, chunk, 1, D, N * D, D);
+    }
     T xr[TPT], zr[TPT], dr[TPT];     // the next tile's values as loaded
     float xk[TPT], zk[TPT], sum = 0.f;
     uint32_t ahead = 0;
@@ -190,7 +200,7 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
         __syncthreads();
         if (ok) {
 #pragma unroll
-            for (int s = 0; s < S; ++s) ch.ends[((k.b * ch.n + chunk) * N + w * S + s) * D + c] = h[s];
+            for (int s = 0; s < S; ++s) ends[(chunk * N + s) * D] = h[s];
             if (w == 0) {
                 float v = 0.f;
 #pragma unroll

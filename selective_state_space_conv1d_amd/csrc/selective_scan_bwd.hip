@@ -150,7 +150,7 @@ __global__ __launch_bounds__(64 * W) void selective_states_kernel(SelBwdArgs a, 
     float A2[S], h[S], p[S], gr[S], dsum = 0.f;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        A2[s] = a.A[static_cast<int64_t>(cs) * N + w * S + s] * kLog2e;
+        A2[s] = base2_rate(a.A[static_cast<int64_t>(cs) * N + w * S + s]);
         h[s] = !SPLIT && a.init_state ? a.init_state[(k.b * D + cs) * N + w * S + s] : 0.f;
         p[s] = 1.f;
         gr[s] = 0.f;
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
         const int64_t so = (b * D + c[j]) * N + w * S;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            A2[j][s] = a.A[static_cast<int64_t>(c[j]) * N + w * S + s] * kLog2e;
+            A2[j][s] = base2_rate(a.A[static_cast<int64_t>(c[j]) * N + w * S + s]);
             dA[j][s] = 0.f;
             carry[j][s] = a.dfinal_state && ok[j] ? a.dfinal_state[so + s] : 0.f;
             if constexpr (SPLIT) hin[j][s] = a.init_state ? a.init_state[so + s] : 0.f;

@@ -233,6 +233,34 @@ def test_values_out_of_range_stay_in_their_place():
     assert all(torch.isfinite(v).all() for v in got.values() if v is not None)
 
 
+@pytest.mark.parametrize("L", [5, 48, 141])
+def test_channel_that_forgets_everything(L):
+    """A of minus infinity: the state is what the last token brought, also where the last tile is not full."""
+    s = make(1, L, 64, 1, 16, F32, 14, gate=False)
+    s["A"][5] = float("-inf")
+    y, final = forward(s)
+    args = [s[k] for k in ARGS] + [s["init"], s["dt_bias"], True]
+    ry, rf, _, _ = ref.scan(*args)
+    my, mf, _, _ = ref.scan(*args, absolute=True)
+    ref.check(y, ry, my, k_of(L, 16), "y")
+    ref.check(final, rf, mf, k_of(L, 16), "final")
+    got = ssd.ssd_selective_scan_bwd(s["dy"], *[s[k] for k in ARGS], init_state=s["init"], dfinal_state=s["dfinal"], dt_bias=s["dt_bias"],
+                                     dt_softplus=True)
+    assert all(torch.isfinite(v).all() for v in got.values() if v is not None)
+
+
+@pytest.mark.parametrize("size", [(2, 700, 136, 1, 16), (1, 400, 72, 1, 64), (40, 130, 64, 1, 16)])
+def test_chunked_scan_in_place(size):
+    """The final state written over the initial one, which the first chunk needs."""
+    s = make(*size, BF, 15)
+    y, final = forward(s)
+    state = s["init"].clone()
+    for _ in range(3):
+        state.copy_(s["init"])
+        y2 = ssd.ssd_selective_scan(*[s[k] for k in ARGS], init_state=state, final_state=state, dt_bias=s["dt_bias"], dt_softplus=True)
+        assert torch.equal(y, y2) and torch.equal(state, final)
+
+
 def test_gradient_is_the_same_every_time_and_on_another_stream():
     s = make(2, 150, 192, 1, 16, BF, 17)
     call = lambda **kw: ssd.ssd_selective_scan_bwd(s["dy"], *[s[k] for k in ARGS], init_state=s["init"], dfinal_state=s["dfinal"],  # noqa: E731
