@@ -231,6 +231,8 @@ __global__ __launch_bounds__(64 * W) void selective_states_kernel(SelBwdArgs a, 
                             if (SPLIT && w == 0) tp[static_cast<int64_t>((u + t) / T) * D] = dsum;
                         }
                     }
+                    // one token after the other: with 16 states a lane, tokens in flight together spill
+                    if constexpr (S >= 16) __builtin_amdgcn_sched_barrier(0);
                     if constexpr (SPLIT) dsum += d[at][t].x;
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
@@ -446,7 +448,10 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
 #pragma unroll
                 for (int s = 0; s < S; ++s) h[j][s] = fmaf(__builtin_amdgcn_exp2f(ts[j] * A2[j][s]), hin[j][s], h[j][s]);
         __syncthreads();
-        float hs[T + 1][P][S], ea[T][P][S];   // states before each token and after the last; decays
+        // states before each token and after the last; decays, which 16 states a lane leave no registers
+        // for: there the way back computes them again
+        constexpr bool KEEP = S < 16;
+        float hs[T + 1][P][S], ea[KEEP ? T : 1][P][S];
 #pragma unroll
         for (int j = 0; j < P; ++j)
 #pragma unroll
@@ -473,8 +478,9 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
                     float y = 0.f;
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
-                        ea[t][j][s] = __builtin_amdgcn_exp2f(d.x * A2[j][s]);
-                        hs[t + 1][j][s] = fmaf(ea[t][j][s], hs[t][j][s], d.y * rows[at].b(v, s));
+                        const float e = __builtin_amdgcn_exp2f(d.x * A2[j][s]);
+                        if constexpr (KEEP) ea[t][j][s] = e;
+                        hs[t + 1][j][s] = fmaf(e, hs[t][j][s], d.y * rows[at].b(v, s));
                         if constexpr (GATE) y = fmaf(hs[t + 1][j][s], rows[at].c(v, s), y);
                     }
                     if constexpr (GATE) ypart[w][t][j][lane] = y;
@@ -512,7 +518,7 @@ __global__ __launch_bounds__(64 * SelGradShape<N>::W, 2) void selective_grad_ker
                         pB[s] = j == 0 ? g * d.y : fmaf(g, d.y, pB[s]);
                         pC[s] = j == 0 ? dy * hs[t + 1][j][s] : fmaf(dy, hs[t + 1][j][s], pC[s]);
                         gB = fmaf(g, rows[at].b(v, s), gB);
-                        carry[j][s] = ea[t][j][s] * g;
+                        carry[j][s] = (KEEP ? ea[KEEP ? t : 0][j][s] : __builtin_amdgcn_exp2f(d.x * A2[j][s])) * g;
                         const float x = carry[j][s] * hs[t][j][s];
                         dA[j][s] = fmaf(d.x, x, dA[j][s]);
                         gA = fmaf(A2[j][s], x, gA);
