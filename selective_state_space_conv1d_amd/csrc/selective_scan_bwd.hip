@@ -226,13 +226,13 @@ __global__ __launch_bounds__(64 * W) void selective_states_kernel(SelBwdArgs a, 
                     if ((u + t) % T == 0 && u + t <= last) {
                         // the state at the start of a tile, and the chunk's sum of dt before it
                         if (ok) {
+                            int64_t row = D;
+                            asm volatile("" : "+s"(row));   // rows' offsets are made here, not kept over the loop
 #pragma unroll
-                            for (int s = 0; s < S; ++s) cp[static_cast<int64_t>((u + t) / T * N + s) * D] = h[s];
-                            if (SPLIT && w == 0) tp[static_cast<int64_t>((u + t) / T) * D] = dsum;
+                            for (int s = 0; s < S; ++s) cp[static_cast<int64_t>((u + t) / T * N + s) * row] = h[s];
+                            if (SPLIT && w == 0) tp[static_cast<int64_t>((u + t) / T) * row] = dsum;
                         }
                     }
-                    // one token after the other: with 16 states a lane, tokens in flight together spill
-                    if constexpr (S >= 16) __builtin_amdgcn_sched_barrier(0);
                     if constexpr (SPLIT) dsum += d[at][t].x;
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
@@ -241,6 +241,8 @@ __global__ __launch_bounds__(64 * W) void selective_states_kernel(SelBwdArgs a, 
                         if constexpr (WITH_G) {
                             p[s] *= e;
                             gr[s] = fmaf(p[s], rows[at].c(t, s) * y[at][t], gr[s]);
+                            // added here and not, as the compiler would have it, after the next tile's stores
+                            asm volatile("" : "+v"(gr[s]));
                         }
                     }
                 }
