@@ -217,11 +217,12 @@ constexpr int sel_waves(int d_state) { return d_state == 128 ? 8 : 4; }
 // in all, the second pass that chunks cost (5/6 of the first one's vector operations) is less than what
 // stands idle.  Measured, 16 states, bf16: 2 x 8192 tokens x 4096 channels (512 waves) 1108 us in one
 // chunk, 616 with 2048 waves, 552 with 3072, 529 with 8192; 1 x 2048 x 4096 277, 84, 79, 83; 8 x 2048 x
-// 4096 (2048 waves) 344 in one chunk, 438 in two.
+// 4096 (2048 waves) 344 in one chunk, 438 in two.  Chunks of 32 tokens or more: 3 x 333 x 768, 32 states,
+// fp32 30 us (40 with 64 tokens or more, 31 with 16), 1 x 1024 x 1536 28 us (30, 40).
 static SelChunks sel_chunks(int64_t batch, int64_t L, int channels, int ngroups, int d_state) {
     const int64_t waves = batch * sel_blocks(channels, ngroups) * sel_waves(d_state);
     int64_t n = waves >= 1024 || waves == 0 ? 1 : (6144 + waves - 1) / waves;
-    if (n > L / 64) n = L / 64 > 0 ? L / 64 : 1;   // a chunk has 64 tokens or more
+    if (n > L / 32) n = L / 32 > 0 ? L / 32 : 1;
     int64_t tokens = (L + n - 1) / n;
     tokens = (tokens + kSelTile - 1) / kSelTile * kSelTile;
     if (n == 1) tokens = L > 0 ? L : 1;

@@ -34,7 +34,9 @@ template <> struct SelGradShape<32> { static constexpr int S = 8, W = 4, CPL = 1
 template <> struct SelGradShape<64> { static constexpr int S = 8, W = 8, CPL = 1, T = 8; };
 template <> struct SelGradShape<128> { static constexpr int S = 16, W = 8, CPL = 1, T = 4; };
 
-// Below this many waves of the gradients launch sequences are cut into chunks.
+// Sequences are cut into chunks up to this many waves of the gradients launch, two for each SIMD, which is
+// what its registers allow; chunks have 32 tokens or more (3 x 333 x 768, 32 states, fp32: 69 us, with 64
+// or more 93, with 16 or more 73; 1 x 512 x 2048: 56, 69, 60).
 constexpr int64_t kGradWaves = 2048;
 
 constexpr int kStatesTile = 16;   // tokens staged at a time by the states launch
@@ -55,7 +57,7 @@ static SelBwdLayout layout_n(int64_t batch, int64_t L, int64_t D, int64_t G) {
     l.blocks = G * ((D / G + 64 * Z::CPL - 1) / (64 * Z::CPL));
     const int64_t waves = batch * l.blocks * Z::W;
     int64_t n = waves >= kGradWaves || waves == 0 ? 1 : (kGradWaves + waves - 1) / waves;
-    if (n > L / 64) n = L / 64 > 0 ? L / 64 : 1;
+    if (n > L / 32) n = L / 32 > 0 ? L / 32 : 1;
     l.tokens = n == 1 ? (L > 0 ? L : 1) : ((L + n - 1) / n + kStatesTile - 1) / kStatesTile * kStatesTile;
     l.chunks = static_cast<int>(L > 0 ? (L + l.tokens - 1) / l.tokens : 1);
     int64_t at = 0;

@@ -39,7 +39,7 @@ def k_of(L, N):
 ARGS = ("x", "dt", "A", "B", "C", "D", "z")
 # batch, tokens, channels, groups, states: one token; a tile's border; channels that end inside a
 # workgroup, groups that do; every state count; several tiles; more than one batch entry
-# (sequences of 128 tokens and more are cut into chunks at these sizes, the last one is not)
+# (sequences of 64 tokens and more are cut into chunks at these sizes, save where the batch fills the chip)
 SIZES = [(1, 140, 72, 1, 32), (1, 130, 40, 2, 64), (2, 133, 66, 1, 128), (512, 130, 8, 1, 16),
          (1, 1, 8, 1, 16), (2, 16, 64, 1, 16), (1, 17, 72, 1, 16), (2, 37, 200, 2, 16), (3, 100, 40, 1, 32),
          (1, 65, 96, 2, 64), (2, 33, 130, 1, 128), (1, 300, 64, 1, 16), (1, 5, 1, 1, 32), (1, 15, 66, 3, 64)]
