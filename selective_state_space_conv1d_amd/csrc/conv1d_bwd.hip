@@ -36,7 +36,7 @@ __global__ __launch_bounds__(kCbLanes * kCbSub) void conv1d_bwd_kernel(ConvBwdAr
     constexpr int V = kCbV;
     typedef T Raw __attribute__((ext_vector_type(V)));
     __shared__ float red[kCbSub][5][V][kCbLanes];
-    const int lane = threadIdx.x % kCbLanes, sub = threadIdx.x / kCbLanes;
+    const int lane = threadIdx.x % kCbLanes, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / kCbLanes);   // a wave's own tile
     const int64_t cb = blockIdx.x % cblocks, tb = blockIdx.x / cblocks % tblocks, b = blockIdx.x / (cblocks * tblocks);
     const int64_t CD = a.channels, L = a.seqlen;
     const bool ok = (cb * kCbLanes + lane) * V < CD;
