@@ -4,11 +4,14 @@
 // The states' own gradients: conv_state_out[k] = u~[L-4+k] adds to du~, and conv_state_in's gradient is
 // du~ at the four positions before the first token (the oldest feeds no output).
 //
-// A thread owns four channels (eight of bf16 would take more registers than two waves a SIMD have) and walks a tile of tokens with the last three inputs
-// and q values in registers, so each input is read once (plus three rows on either side of a tile) and
-// each output written once: bound by HBM.  Rows are taken four at a time, the next four loaded while
-// four are computed.  dw and dbias are summed in registers over the tile, over the workgroup's tiles
-// in LDS and over workgroups by a second launch, in a fixed order.
+// A thread owns four channels (eight of bf16 would take more registers than two waves a SIMD have) and walks
+// a tile of tokens with the last three inputs and q values in registers, so each input is read once (plus
+// three rows on either side of a tile) and each output written once: bound by HBM.  Rows are taken four at a
+// time, the next four loaded while four are computed.  dw and dbias are summed in registers over the tile,
+// over the workgroup's tiles in LDS and over workgroups by a second launch, in a fixed order.
+// 2 x 8192 x 18432, bf16: 378 us back to back, 4.8 TB/s of its 1.81 GB (a device copy: 5.2); 4 x 2048 x 8192:
+// 97 us; 1 x 77 x 1792, fp32: 12 + 4 us, the chain of a tile's 16 rows.  Held to three waves a SIMD by its
+// register count the first takes 481 us, with ordinary stores in place of non-temporal ones 420.
 #include "ssd_device.h"
 #include "ssd_kernels.h"
 
@@ -21,8 +24,8 @@ constexpr int kCbLanes = 64;      // threads across the channels of a workgroup
 constexpr int kCbSub = 4;         // token tiles per workgroup, one for each wave
 
 // Rows that a tile walks, its tokens and the three after them: 128, fewer where that gives less than two
-// workgroups a CU (2 x 8192 x 18432, bf16: 408 us with 128, 440 with 64, 422 with 256; 1 x 8192 x 18432: 204,
-// 207, 241).
+// workgroups a CU (with an earlier form of the loop, 2 x 8192 x 18432, bf16: 408 us with 128, 440 with 64, 422
+// with 256; 1 x 8192 x 18432: 204, 207, 241).
 static int64_t tile_steps(int64_t batch, int64_t L, int64_t CD) {
     const int64_t cb = (CD + kCbLanes * kCbV - 1) / (kCbLanes * kCbV);
     int64_t steps = 128;

@@ -14,10 +14,11 @@ constexpr int64_t kPoolSpan = static_cast<int64_t>(kPoolThreads) * kPoolFlight *
 // Entries take effect in their order: an entry whose source is an earlier entry's destination copies
 // what that entry left, and of two entries with one destination the later one stays.  Workgroups that
 // each copy one entry keep to that when no destination occurs twice and none is another entry's
-// source.  Every workgroup tests this on a bitmap of the destinations (slot mod 8192: slots that share a
+// source.  Every workgroup tests this on a bitmap of the destinations (slot mod 131072: slots that share a
 // bit count as equal, which is on the safe side); when the test fails the workgroups of entry 0 copy
-// all entries one after the other, each thread its own bytes, and the others leave.
-constexpr int kPoolBits = 8192;
+// all entries one after the other, each thread its own bytes, and the others leave.  The bitmap takes
+// 16 KiB of LDS, which leaves room for the eight workgroups that a CU holds.
+constexpr int kPoolBits = 131072;
 
 __global__ __launch_bounds__(kPoolThreads) void pool_copy_kernel(PoolCopyArgs a, int64_t spans) {
     __shared__ uint32_t seen[kPoolBits / 32];
@@ -33,7 +34,8 @@ __global__ __launch_bounds__(kPoolThreads) void pool_copy_kernel(PoolCopyArgs a,
         return s >= 0 && s < a.src_slots ? s : -1;
     };
     if (a.src && a.n > 1) {   // clearing a slot twice clears it
-        for (int i = threadIdx.x; i < kPoolBits / 32; i += kPoolThreads) seen[i] = 0;
+        const int words = static_cast<int>(((a.dst_slots < kPoolBits ? a.dst_slots : kPoolBits) + 31) / 32);
+        for (int i = threadIdx.x; i < words; i += kPoolThreads) seen[i] = 0;
         if (threadIdx.x == 0) ordered = 0;
         __syncthreads();
         bool bad = false;
@@ -47,7 +49,7 @@ __global__ __launch_bounds__(kPoolThreads) void pool_copy_kernel(PoolCopyArgs a,
         if (same)
             for (int64_t e = threadIdx.x; e < a.n; e += kPoolThreads) {
                 const int64_t d = dst_of(e), s = src_of(e);
-                if (d < 0 || s < 0 || d == s) continue;
+                if (d < 0 || s < 0 || d == s || s >= a.dst_slots) continue;   // past dst's slots: nobody's destination
                 bad |= (seen[(s % kPoolBits) / 32] >> (s & 31) & 1u) != 0;
             }
         if (bad) ordered = 1;

@@ -53,7 +53,7 @@ def test_copy_between_pools_of_layers(pair):
 
 
 def test_copy_of_many_entries():
-    """More entries than threads and than bits of the duplicates' bitmap's words; slots that share a bit."""
+    """More entries than threads; slots whose numbers agree in many low bits."""
     pool = rand(20000, 4)
     g = torch.Generator().manual_seed(5)
     p = torch.randperm(20000, generator=g)
@@ -63,10 +63,33 @@ def test_copy_of_many_entries():
     got = pool.to(DEV)
     ssd.ssd_pool_copy(got, i32(di), got, i32(si))
     assert torch.equal(got.cpu(), want)
-    got = pool.to(DEV)                              # slots 8192 apart share a bit: one after the other
+    got = pool.to(DEV)
     ssd.ssd_pool_copy(got, i32([8192, 0, 16384]), got, i32([5, 6, 7]))
     want = pool.clone()
     want[[8192, 0, 16384]] = pool[[5, 6, 7]]
+    assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("di,si", [([131077, 5, 262149, 9], [1, 2, 3, 4]),           # destinations that share a bit
+                                   ([4, 131081, 7], [262153, 9, 131076]),            # a source that shares one
+                                   ([131072, 299999, 131071], [299999, 131072, 0]),  # the last bit and the first; a swap
+                                   ([299999, -1, 300000], [131072, 299999, 5])])
+def test_pools_of_more_slots_than_the_bitmap_has_bits(di, si):
+    pool = rand(300000, 4)
+    want = pool.clone()
+    host_copy(want, di, want, si, 0)
+    got = pool.to(DEV)
+    ssd.ssd_pool_copy(got, i32(di), got, i32(si))
+    assert torch.equal(got.cpu(), want)
+
+
+def test_source_slots_past_the_destinations():
+    """One pool named twice, as destination by its first 40 slots only."""
+    pool = rand(100, 4)
+    want = pool.clone()
+    host_copy(want[:40], [39, 7, 8, 41], want, [99, 64, 32, 3], 0)
+    got = pool.to(DEV)
+    ssd.ssd_pool_copy(got[:40], i32([39, 7, 8, 41]), got, i32([99, 64, 32, 3]))
     assert torch.equal(got.cpu(), want)
 
 
