@@ -571,8 +571,8 @@ ssd_status_t ssd_conv1d_update_accept(const ssd_dims_t* d, const void* xbc, int6
 /*
  * Scan of a prefill.
  *  x, z         [B, L, D] act dtype; token rows x_row_stride / z_row_stride elements apart (>= D),
- *               batch rows L rows apart; D and row strides are at most 2^24.  x may be the conv's output, z a view into in_proj's.  z may
- *               be NULL (no gate; its stride is then not read).
+ *               batch rows L rows apart; D and row strides are at most 2^24.  x may be the conv's
+ *               output, z a view into in_proj's.  z may be NULL (no gate; its stride is then not read).
  *  dt           [B, L, D] contiguous act dtype.  dt_params as for ssd_chunk_scan, bias [D].
  *  A            [D, N] fp32.  Dskip: [D] fp32 or NULL.
  *  B, C         B[b,t,g,n] at B[(b*L + t)*bc_row_stride + g*N + n] (same for C); act dtype, 16-byte
@@ -582,7 +582,9 @@ ssd_status_t ssd_conv1d_update_accept(const ssd_dims_t* d, const void* xbc, int6
  *               may alias init_state.
  *  y            [B, L, D] contiguous, y dtype.
  *  workspace    as many bytes as ssd_selective_scan_workspace_size() returns, 16-byte aligned,
- *               overwritten (may be NULL when that is 0; smaller: SSD_ERR_WORKSPACE).
+ *               overwritten (may be NULL when that is 0; smaller: SSD_ERR_WORKSPACE).  Calls that may
+ *               run at the same time need one each, captured ones too.
+ * y and final_state must not overlap the inputs, but for final_state = init_state.
  */
 size_t ssd_selective_scan_workspace_size(const ssd_dims_t* d);
 ssd_status_t ssd_selective_scan(const ssd_dims_t* d, const void* x, int64_t x_row_stride, const void* dt,
@@ -600,7 +602,8 @@ ssd_status_t ssd_selective_scan(const ssd_dims_t* d, const void* x, int64_t x_ro
  *  dB, dC        [B, L, G, N] contiguous act dtype.
  *  dA [D, N], dDskip [D], ddt_bias [D], dinit_state [B, D, N]: fp32; dDskip, ddt_bias and dinit_state
  *                may be NULL (not written).
- * Every gradient is overwritten, and is the same bit for bit on every call with the same inputs.
+ * Every gradient is overwritten, and is the same bit for bit on every call with the same inputs.  The
+ * gradients must not overlap the inputs or one another.
  * Sums over tokens and channels are fp32.  The rest is as for ssd_selective_scan; a workspace of
  * ssd_selective_scan_bwd_workspace_size() bytes is required.
  */
