@@ -12,9 +12,9 @@
 //
 // Bound: the vector pipe.  A state of a token and channel takes six issue slots (a product, an exp2 of two
 // slots, a product and two fmas) of four cycles for 64 lanes; no product shares an operand across channels, so
-// the matrix pipe does not apply.  2 x 8192 tokens x 4096 channels, 16 states, bf16, z and states: 203 us
-// (chunk states, five slots) + 311 us under the profiler, of which the states' slots take 125 and 164 and the
-// tokens' own work (dt's softplus, gate, sums over waves) 40 and 85; 463 us back to back.
+// the matrix pipe does not apply.  2 x 8192 tokens x 4096 channels, 16 states, bf16, z and states: 199 us
+// (chunk states, five slots) + 277 us under the profiler, of which the states' slots take 128 and 164 and the
+// tokens' own work (dt's softplus, gate, sums over waves) 40 and 85; 417 us back to back.
 #include "selective_device.h"
 
 namespace ssd {
@@ -38,8 +38,10 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
     constexpr int N = S * W, TPT = kSelTile / W;   // tokens of a tile that one thread stages
     constexpr int SUB = SelRows<T, S>::n;          // tokens whose B and C are in scalar registers
     constexpr int E = sizeof(T);
-    __shared__ float2 st[2][kSelTile][64];         // dt, dt * x
-    __shared__ float part[Y ? 2 : 1][Y ? W : 1][kSelTile][64];
+    // dt, dt * x; twice without y, which saves a barrier.  With y the waves that less LDS lets in are worth
+    // more than the barrier (2 x 8192 x 4096, bf16: 484 us; both arrays twice, one barrier a tile: 514)
+    __shared__ float2 st[Y ? 1 : 2][kSelTile][64];
+    __shared__ float part[Y ? W : 1][kSelTile][64];   // y of the wave's states
     const int64_t per_chunk = a.batch * sel_blocks(a.channels, a.ngroups);
     const int chunk = static_cast<int>(blockIdx.x / per_chunk);
     const SelBlock k = sel_block(blockIdx.x % per_chunk, a.channels, a.ngroups);
@@ -101,16 +103,16 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
         const uint32_t t = static_cast<uint32_t>(first + (lane & 15) < last ? first + (lane & 15) : last);
         ahead = *reinterpret_cast<const uint32_t*>((lane & 16 ? Cp : Bp) + static_cast<uint64_t>(t * bs));
     };
-    // y of the tile before the one that starts at yp, whose partial sums lie in part[buf]; rows past
-    // `last` of it do not exist
-    auto finish = [&](int buf, int last) {
+    // y of the tile before the one that starts at yp, whose partial sums lie in part; rows past `last` of
+    // it do not exist
+    auto finish = [&](int last) {
         if constexpr (Y) {
             float y[TPT];
 #pragma unroll
             for (int i = 0; i < TPT; ++i) {
                 y[i] = Dv * xk[i];
 #pragma unroll
-                for (int v = 0; v < W; ++v) y[i] += part[buf][v][w + W * i][lane];
+                for (int v = 0; v < W; ++v) y[i] += part[v][w + W * i][lane];
                 if constexpr (GATE) y[i] *= silu_f(zk[i]);
             }
             char* base = yp - static_cast<int64_t>(kSelTile) * ys;
@@ -134,7 +136,7 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
         rows[0].template load<Y>(Bp, Cp, bs, 0, L - 1);
     }
     int buf = 0;
-    for (int t0 = 0; t0 < L; t0 += kSelTile, buf ^= 1) {
+    for (int t0 = 0; t0 < L; t0 += kSelTile, buf ^= Y ? 0 : 1) {
         const int last = L - 1 - t0;
         float xn[TPT], dn[TPT], zn[TPT];
 #pragma unroll
@@ -149,6 +151,10 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
 #pragma unroll
             for (int i = 0; i < TPT; ++i)
                 if (w + W * i > last) xn[i] = dn[i] = 0.f;
+        if constexpr (Y) {
+            __syncthreads();
+            if (t0 > 0) finish(kSelTile);
+        }
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
             st[buf][w + W * i][lane] = make_float2(dn[i], dn[i] * xn[i]);
@@ -158,7 +164,6 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
         load(kSelTile, last);
 #pragma unroll
         for (int t = 0; t < SUB; ++t) d[0][t] = st[buf][t][lane];
-        if (t0 > 0) finish(buf ^ 1, kSelTile);
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
             xk[i] = xn[i];
@@ -182,7 +187,7 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
                     h[s] = fmaf(e, h[s], d[at][t].y * rows[at].b(t, s));
                     if constexpr (Y) y = fmaf(h[s], rows[at].c(t, s), y);
                 }
-                if constexpr (Y) part[buf][w][u + t][lane] = y;
+                if constexpr (Y) part[w][u + t][lane] = y;
             }
         }
         xp += static_cast<int64_t>(kSelTile) * xs;
@@ -194,7 +199,7 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
     }
     __syncthreads();
     if constexpr (Y) {
-        if (L > 0) finish(buf ^ 1, (L - 1) % kSelTile);
+        if (L > 0) finish((L - 1) % kSelTile);
         if (a.final_state && ok && chunk == ch.n - 1) {
 #pragma unroll
             for (int s = 0; s < S; ++s) a.final_state[so + s] = h[s];
@@ -217,15 +222,15 @@ __global__ __launch_bounds__(64 * W) void selective_scan_kernel(SelScanArgs a, S
 
 constexpr int sel_waves(int d_state) { return d_state == 128 ? 8 : 4; }
 
-// Chunks of a sequence.  The kernel wants three waves or more on each of the 1024 SIMDs; below 1024 waves
+// Chunks of a sequence.  The kernel wants three waves or more on each of the 1024 SIMDs; below 2048 waves
 // in all, the second pass that chunks cost (5/6 of the first one's vector operations) is less than what
 // stands idle.  Measured, 16 states, bf16: 2 x 8192 tokens x 4096 channels (512 waves) 1108 us in one
-// chunk, 616 with 2048 waves, 552 with 3072, 529 with 8192; 1 x 2048 x 4096 277, 84, 79, 83; 8 x 2048 x
-// 4096 (2048 waves) 344 in one chunk, 438 in two.  Chunks of 32 tokens or more: 3 x 333 x 768, 32 states,
-// fp32 30 us (40 with 64 tokens or more, 31 with 16), 1 x 1024 x 1536 28 us (30, 40).
+// chunk, 499 with 5120 waves, 490 with 6144, 484 with 8192, 490 with 12288; 6 x 2048 x 4096 (1536 waves) 338
+// in one chunk, 303 in six; 8 x 2048 x 4096 (2048 waves) 341-366 in one, 450 in four.  Chunks of 32 tokens
+// or more: 1 x 512 x 4096 29 us (38 with 16 tokens or more), 1 x 1024 x 1536 28 (37; 40 with 64).
 static SelChunks sel_chunks(int64_t batch, int64_t L, int channels, int ngroups, int d_state) {
     const int64_t waves = batch * sel_blocks(channels, ngroups) * sel_waves(d_state);
-    int64_t n = waves >= 1024 || waves == 0 ? 1 : (6144 + waves - 1) / waves;
+    int64_t n = waves >= 2048 || waves == 0 ? 1 : (8192 + waves - 1) / waves;
     if (n > L / 32) n = L / 32 > 0 ? L / 32 : 1;
     int64_t tokens = (L + n - 1) / n;
     tokens = (tokens + kSelTile - 1) / kSelTile * kSelTile;
