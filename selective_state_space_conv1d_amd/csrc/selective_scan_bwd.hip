@@ -28,6 +28,7 @@
 // its time to waits.
 #include "selective_device.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace ssd {
@@ -39,12 +40,36 @@ template <> struct SelGradShape<32> { static constexpr int S = 8, W = 4, CPL = 1
 template <> struct SelGradShape<64> { static constexpr int S = 8, W = 8, CPL = 1, T = 8; };
 template <> struct SelGradShape<128> { static constexpr int S = 16, W = 8, CPL = 1, T = 4; };
 
-// Sequences are cut into chunks up to this many waves of the gradients launch, two for each SIMD, which is
-// what its registers allow; chunks have 32 tokens or more (3 x 333 x 768, 32 states, fp32: 69 us, with 64
-// or more 93, with 16 or more 73; 1 x 512 x 2048: 56, 69, 60).
+// Waves of the gradients launch that run at once: two for each SIMD, which is what its registers allow.
 constexpr int64_t kGradWaves = 2048;
 
 constexpr int kStatesTile = 16;   // tokens staged at a time by the states launch
+
+// Tokens of a chunk (all L: one chunk) for `waves` waves a chunk.  One chunk takes as many rounds of
+// kGradWaves as it has, of which a last one that is not full takes 0.55 to 1; chunks take a tenth more work
+// and some tokens' time each, and are made so many that they fill whole rounds, one to five.  Measured, 16
+// states, bf16, 4096 channels (128 waves for each batch entry): 6 x 2048 tokens 855 us in 5 chunks (1122 in 3,
+// which is 1.1 rounds), 10 x 2048 1392 in 8 (1844 in one), 17 x 1024 1227 in 4 (1512 in one), 24 x 1024 1576
+// in one (1602 in 2).  Chunks have 32 tokens or more (3 x 333 x 768, 32 states, fp32: 69 us, with 64 or more
+// 93, with 16 or more 73; 1 x 512 x 2048: 56, 69, 60).
+static int64_t grad_chunk_tokens(int64_t waves, int64_t L) {
+    int64_t best = L > 0 ? L : 1;
+    const double last = static_cast<double>(waves % kGradWaves) / kGradWaves;
+    const double one = waves <= kGradWaves ? 1. : waves / kGradWaves + (last > 0. ? std::max(0.55, 0.2 + 0.8 * last) : 0.);
+    double least = one * (best + 16);
+    for (int rounds = 1; waves > 0 && rounds <= 5; ++rounds) {
+        int64_t n = rounds * kGradWaves / waves;
+        if (n > L / 32) n = L / 32;
+        if (n < 2) continue;
+        const int64_t tokens = ((L + n - 1) / n + kStatesTile - 1) / kStatesTile * kStatesTile;
+        const double cost = 1.1 * rounds * (tokens + 16);
+        if (cost < least) {
+            least = cost;
+            best = tokens;
+        }
+    }
+    return best;
+}
 
 // Offsets in floats of the workspace's parts, and the chunks.
 struct SelBwdLayout {
@@ -60,10 +85,7 @@ static SelBwdLayout layout_n(int64_t batch, int64_t L, int64_t D, int64_t G) {
     SelBwdLayout l;
     l.tiles = (L + Z::T - 1) / Z::T;
     l.blocks = G * ((D / G + 64 * Z::CPL - 1) / (64 * Z::CPL));
-    const int64_t waves = batch * l.blocks * Z::W;
-    int64_t n = waves >= kGradWaves || waves == 0 ? 1 : (kGradWaves + waves - 1) / waves;
-    if (n > L / 32) n = L / 32 > 0 ? L / 32 : 1;
-    l.tokens = n == 1 ? (L > 0 ? L : 1) : ((L + n - 1) / n + kStatesTile - 1) / kStatesTile * kStatesTile;
+    l.tokens = grad_chunk_tokens(batch * l.blocks * Z::W, L);
     l.chunks = static_cast<int>(L > 0 ? (L + l.tokens - 1) / l.tokens : 1);
     int64_t at = 0;
     auto take = [&](int64_t n) {
