@@ -12,9 +12,9 @@
 //
 // Bound: the vector pipe.  A state of a token and channel takes six issue slots (a product, an exp2 of two
 // slots, a product and two fmas) of four cycles for 64 lanes; no product shares an operand across channels, so
-// the matrix pipe does not apply.  2 x 8192 tokens x 4096 channels, 16 states, bf16, z and states: 199 us
-// (chunk states, five slots) + 277 us under the profiler, of which the states' slots take 128 and 164 and the
-// tokens' own work (dt's softplus, gate, sums over waves) 40 and 85; 417 us back to back.
+// the matrix pipe does not apply.  2 x 8192 tokens x 4096 channels, 16 states, bf16, z and states: 196 us
+// (chunk states, five slots) + 273 us under the profiler, of which the states' slots take 128 and 164 and the
+// tokens' own work (dt's softplus, gate, sums over waves) 40 and 85; 411 us back to back.
 #include "selective_device.h"
 
 namespace ssd {

@@ -24,7 +24,7 @@
 //
 // Bound: the vector pipe, about 21 issue slots of a state of a token and channel in (2), seven in (1), and
 // the tokens' own work.  4 x 2048 tokens x 4096 channels, 16 states, bf16: 183 + 425 + 10 us under the
-// profiler, 573 us back to back; the registers allow (2) two waves a SIMD, which leaves about a quarter of
+// profiler, 572 us back to back; the registers allow (2) two waves a SIMD, which leaves about a quarter of
 // its time to waits.
 #include "selective_device.h"
 
