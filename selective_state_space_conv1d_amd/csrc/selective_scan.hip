@@ -231,7 +231,7 @@ constexpr int sel_waves(int d_state) { return d_state == 128 ? 8 : 4; }
 static SelChunks sel_chunks(int64_t batch, int64_t L, int channels, int ngroups, int d_state) {
     const int64_t waves = batch * sel_blocks(channels, ngroups) * sel_waves(d_state);
     int64_t n = waves >= 2048 || waves == 0 ? 1 : (8192 + waves - 1) / waves;
-    if (n > L / 32) n = L / 32 > 0 ? L / 32 : 1;
+    if (n > most_chunks(L)) n = most_chunks(L);
     int64_t tokens = (L + n - 1) / n;
     tokens = (tokens + kSelTile - 1) / kSelTile * kSelTile;
     if (n == 1) tokens = L > 0 ? L : 1;

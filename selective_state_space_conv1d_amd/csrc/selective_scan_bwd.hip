@@ -59,7 +59,7 @@ static int64_t grad_chunk_tokens(int64_t waves, int64_t L) {
     double least = one * (best + 16);
     for (int rounds = 1; waves > 0 && rounds <= 5; ++rounds) {
         int64_t n = rounds * kGradWaves / waves;
-        if (n > L / 32) n = L / 32;
+        if (n > most_chunks(L)) n = most_chunks(L);
         if (n < 2) continue;
         const int64_t tokens = ((L + n - 1) / n + kStatesTile - 1) / kStatesTile * kStatesTile;
         const double cost = 1.1 * rounds * (tokens + 16);
