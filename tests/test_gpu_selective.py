@@ -42,7 +42,8 @@ ARGS = ("x", "dt", "A", "B", "C", "D", "z")
 # (sequences of 64 tokens and more are cut into chunks at these sizes, save where the batch fills the chip)
 SIZES = [(1, 140, 72, 1, 32), (1, 130, 40, 2, 64), (2, 133, 66, 1, 128), (512, 130, 8, 1, 16),
          (1, 1, 8, 1, 16), (2, 16, 64, 1, 16), (1, 17, 72, 1, 16), (2, 37, 200, 2, 16), (3, 100, 40, 1, 32),
-         (1, 65, 96, 2, 64), (2, 33, 130, 1, 128), (1, 300, 64, 1, 16), (1, 5, 1, 1, 32), (1, 15, 66, 3, 64)]
+         (1, 65, 96, 2, 64), (2, 33, 130, 1, 128), (1, 300, 64, 1, 16), (1, 5, 1, 1, 32), (1, 15, 66, 3, 64),
+         (1, 1500, 24, 1, 16)]                      # more chunks of 32 tokens than the root of the length
 
 
 def forward(s, **kw):
